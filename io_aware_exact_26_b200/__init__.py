@@ -31,3 +31,12 @@ from .binding import (  # noqa: F401
     lib,
     library_path,
 )
+from .paged import (  # noqa: F401
+    attn_cache_read,
+    attn_cache_write,
+    attn_paged,
+    attn_paged_workspace_size,
+    attn_rope,
+    attn_rope_bwd,
+    rope_inv_freq,
+)

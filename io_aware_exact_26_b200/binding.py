@@ -100,7 +100,8 @@ def load(path):
     L.attn_selftest_bounds.restype = i
     L.attn_selftest_sched.argtypes = [vp, vp]
     L.attn_selftest_sched.restype = i
-    return L
+    from . import paged          # the serving operators' entry points (include/attn_paged.h)
+    return paged.declare(L)
 
 
 def attn_status_string(status: int) -> str:

@@ -12,6 +12,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "attn.h"
 #include "fwd.cuh"
@@ -354,6 +355,8 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
 
 }  // namespace attn
 
+#include "paged_api.cuh"
+
 // ---------------------------------------------------------------------------
 // Scratch for attn_bwd_noalloc: a fixed device array that this library owns, so
 // callers that cannot allocate device memory can still run the backward.  Every
@@ -652,7 +655,15 @@ int attn_get_device_status(void* stream) {
   if (cudaMemcpyFromSymbol(&v, attn::g_attn_status, sizeof(int)) != cudaSuccess) return ATTN_ERR_LAUNCH;
   if (v != 0 && cudaMemcpyToSymbol(attn::g_attn_status, &zero, sizeof(int)) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
-  return v == 0 ? ATTN_OK : v == 2 ? ATTN_ERR_DEVICE_BOUNDS : v == 3 ? ATTN_ERR_SCHED_CONFLICT
+  if (v == 0) {
+    // bad page table entries are recorded in a word of their own, which stops no kernel
+    int bad = 0;
+    if (cudaMemcpyFromSymbol(&bad, attn::g_attn_bad_page, sizeof(int)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+    if (bad == 0) return ATTN_OK;
+    if (cudaMemcpyToSymbol(attn::g_attn_bad_page, &zero, sizeof(int)) != cudaSuccess) return ATTN_ERR_LAUNCH;
+    return ATTN_ERR_DEVICE_PAGE;
+  }
+  return v == 2 ? ATTN_ERR_DEVICE_BOUNDS : v == 3 ? ATTN_ERR_SCHED_CONFLICT
                                                                        : ATTN_ERR_DEVICE_TIMEOUT;
 }
 
@@ -676,6 +687,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_DEVICE_BOUNDS: return "a device-side index check failed (checking build)";
     case ATTN_ERR_SCHED_CONFLICT:
       return "a launch's work counter was taken over by a later launch (over 128 in flight); both outputs are incomplete";
+    case ATTN_ERR_DEVICE_PAGE: return "a block table entry or a position was outside the page pool";
     default: return "unknown status";
   }
 }

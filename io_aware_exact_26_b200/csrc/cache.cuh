@@ -1,0 +1,452 @@
+// Rotary positions, and the paged K/V cache's write and read-back, for sm_100a.
+//
+// All three are streams: every input element is read once and every output element
+// written once, with a few operations in between, so HBM bounds them at large sizes and
+// the chain launch -> dependent loads -> store at small ones.
+//
+// Rotation.  Pair i of a row is turned by pos * f_i.  The angle of a far position needs
+// more bits than fp32 has (pos = 10^6: an fp32 product is off by 0.03 rad), so a thread
+// forms it in turns, r = pos * (f_i / 2 pi), in fp64, subtracts the nearest integer
+// (exact) and hands |r| <= 1/2 to sincospif in fp32.  Sine and cosine depend on the token
+// and the pair only: a thread owns one 16-byte unit of a token's rows -- for the half
+// layout the chunk of first elements and the chunk of its partners -- and applies the
+// same registers to every head it visits.
+#pragma once
+#include "sm100.cuh"
+
+namespace attn {
+
+// Set when a block table entry or a position lies outside the page pool.  Apart from
+// g_attn_status on purpose: the kernels go on (the access is skipped), so nothing that
+// waits has to give up.
+__device__ int g_attn_bad_page = 0;
+__device__ __forceinline__ void record_bad_page() { atomicExch(&g_attn_bad_page, 1); }
+
+struct RowView {              // [batch][head][token][d], strides in elements
+  char* p;
+  long long sb, sh, st;
+};
+
+struct RopeParams {
+  RowView q, qo, k, ko;       // k.p may be null with Hk = 0
+  int Hq, Hk, B, N;
+  const int* pos;
+  long long pos_sb;
+  const double* inv_freq;
+  int rot, inverse;
+  float mscale;
+  int heads_per_block;        // heads that one block walks through
+};
+
+// 16 bytes of T as floats and back; bf16 rounds to nearest even.
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void load(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 store(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec16<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void load(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 store(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+// How a row of D elements of T is cut into the units that threads own.
+//   half layout: unit u < rot / 2n holds chunks u and u + rot / 2n (n pairs); the copied
+//     rest is cut the same way, into pairs of chunks
+//   interleaved: unit u is chunk u, n / 2 pairs (or n copied elements)
+// Chunks are 16 bytes (n elements), so a warp's accesses are contiguous in both layouts.
+template <typename T, int D, bool INTER>
+struct RopeUnit {
+  static constexpr int n = Vec16<T>::n;
+  static constexpr int kChunks = D / n;                    // per row
+  static constexpr int kUnits = INTER ? kChunks : kChunks / 2;
+  static constexpr int kPairs = INTER ? n / 2 : n;
+  static constexpr int NC = INTER ? 1 : 2;                 // chunks per unit
+  int c0, c1, pair0;
+  bool turned;
+  __device__ __forceinline__ RopeUnit(int u, int rot) {
+    if constexpr (INTER) {
+      c0 = c1 = u;
+      turned = u * n < rot;
+      pair0 = u * kPairs;
+    } else {
+      const int ru = rot / (2 * n);                        // turned units
+      turned = u < ru;
+      const int tail = (kChunks - 2 * ru) / 2;             // copied units
+      c0 = turned ? u : 2 * ru + (u - ru);
+      c1 = turned ? u + ru : c0 + tail;
+      pair0 = u * n;
+    }
+  }
+};
+
+template <int P>
+__device__ __forceinline__ void rope_sincos(const double* __restrict__ inv_freq, int pair0, int pos, float m,
+                                            int inverse, float (&cs)[P], float (&sn)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const double r = static_cast<double>(pos) * (inv_freq[pair0 + i] * 0.15915494309189533577);   // turns
+    const float x = static_cast<float>(r - rint(r));
+    float s, c;
+    sincospif(2.f * x, &s, &c);
+    cs[i] = c * m;
+    sn[i] = inverse ? -s * m : s * m;
+  }
+}
+
+// y = m R x on one unit's registers: a[] is the first chunk, b[] its partner chunk (half
+// layout) or unused (interleaved).
+template <typename T, bool INTER, int P, int n>
+__device__ __forceinline__ void rope_turn(float (&a)[n], float (&b)[n], const float (&cs)[P], const float (&sn)[P]) {
+  if constexpr (INTER) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float x = a[2 * i], y = a[2 * i + 1];
+      a[2 * i] = x * cs[i] - y * sn[i];
+      a[2 * i + 1] = y * cs[i] + x * sn[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = x * cs[i] - y * sn[i];
+      b[i] = y * cs[i] + x * sn[i];
+    }
+  }
+}
+
+// Grid: x over blocks of tokens (256 / kUnits tokens each), y over blocks of heads.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(256) attn_rope_kernel(const RopeParams p) {
+  using U = RopeUnit<T, D, INTER>;
+  constexpr int n = U::n;
+  const int u = threadIdx.x % U::kUnits;
+  const long long tok = static_cast<long long>(blockIdx.x) * (256 / U::kUnits) + threadIdx.x / U::kUnits;
+  if (tok >= static_cast<long long>(p.B) * p.N) return;
+  const int b = static_cast<int>(tok / p.N), t = static_cast<int>(tok - static_cast<long long>(b) * p.N);
+  const U unit(u, p.rot);
+  float cs[U::kPairs], sn[U::kPairs];
+  if (unit.turned)
+    rope_sincos<U::kPairs>(p.inv_freq, unit.pair0, p.pos[b * p.pos_sb + t], p.mscale, p.inverse, cs, sn);
+  const int h0 = blockIdx.y * p.heads_per_block;
+  const int h1 = min(h0 + p.heads_per_block, p.Hq + p.Hk);
+  auto src = [&](int h, int c) -> const uint4* {
+    const RowView& v = h < p.Hq ? p.q : p.k;
+    const int hh = h < p.Hq ? h : h - p.Hq;
+    return reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(v.p) + b * v.sb + hh * v.sh + t * v.st + c * n);
+  };
+  auto dst = [&](int h, int c) -> uint4* {
+    const RowView& v = h < p.Hq ? p.qo : p.ko;
+    const int hh = h < p.Hq ? h : h - p.Hq;
+    return reinterpret_cast<uint4*>(reinterpret_cast<T*>(v.p) + b * v.sb + hh * v.sh + t * v.st + c * n);
+  };
+  constexpr int UN = 4;                       // heads in flight: 64 or 128 bytes per thread
+  for (int h = h0; h < h1; h += UN) {
+    uint4 x[UN][U::NC];
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      if (h + i < h1) {
+        x[i][0] = *src(h + i, unit.c0);
+        if constexpr (U::NC == 2) x[i][1] = *src(h + i, unit.c1);
+      }
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      if (h + i < h1) {
+        if (unit.turned) {
+          float a[n], bb[n];
+          Vec16<T>::load(x[i][0], a);
+          if constexpr (U::NC == 2) Vec16<T>::load(x[i][1], bb);
+          rope_turn<T, INTER, U::kPairs, n>(a, bb, cs, sn);
+          x[i][0] = Vec16<T>::store(a);
+          if constexpr (U::NC == 2) x[i][1] = Vec16<T>::store(bb);
+        }
+        *dst(h + i, unit.c0) = x[i][0];
+        if constexpr (U::NC == 2) *dst(h + i, unit.c1) = x[i][1];
+      }
+  }
+}
+
+// ------------------------------------------------------------------ cache write
+struct CacheView {
+  char* k;
+  char* v;
+  uint8_t* ks;
+  uint8_t* vs;
+  long long page_bytes;       // between pages of k and of v
+  int num_pages, page_shift, Hkv;
+};
+
+struct WriteParams {
+  CacheView c;
+  RowView k, v, q, qo;        // packed rows, bf16
+  int Hq;                     // 0: no queries
+  const int* cu_q;
+  const int* kv_len;
+  const int* table;
+  int B, T, max_pages;
+  const double* inv_freq;     // null: no rotation
+  int rot;
+  float mscale;
+  int heads_per_block;
+};
+
+// Sequence of packed row t: the number of boundaries cu_q[1..B] at or below it (B: padding
+// behind the last sequence).  The warp counts 32 boundaries per step, for the tokens of
+// all its lanes at once: loads that do not depend on one another, where a binary search
+// would wait for one after the other.
+template <int LANES>          // lanes per token, consecutive
+__device__ __forceinline__ int find_sequence(const int* __restrict__ cu_q, int B, int t, int lane) {
+  int cnt = 0;
+  for (int j0 = 0; j0 < B; j0 += 32) {
+    const int e = j0 + lane < B ? cu_q[1 + j0 + lane] : 0x7fffffff;
+#pragma unroll
+    for (int g = 0; g < 32 / LANES; ++g) {
+      const int tg = __shfl_sync(0xffffffffu, t, g * LANES);
+      const unsigned m = __ballot_sync(0xffffffffu, e <= tg);
+      if (lane / LANES == g) cnt += __popc(m);
+    }
+    if (__all_sync(0xffffffffu, __shfl_sync(0xffffffffu, e, 31) > t)) break;
+  }
+  return cnt;
+}
+
+// Exponent of an e4m3 row's power-of-two scale: the smallest e with amax <= 448 * 2^e
+// (448 = 1.75 * 2^8), at least -127.
+__device__ __forceinline__ int e4m3_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < -127 ? -127 : e;
+}
+
+// Grid: x over blocks of tokens, y over blocks of heads; heads 0 .. Hq-1 are queries, then
+// Hkv of K, then Hkv of V.  Lanes of one row are consecutive, so a row's maximum is a few
+// shuffles.  Rows of one warp differ in their heads only by the loop, never by the lane.
+template <int D, bool E4M3, bool INTER>
+__global__ void __launch_bounds__(256) attn_cache_write_kernel(const WriteParams p) {
+  using T = __nv_bfloat16;
+  using U = RopeUnit<T, D, INTER>;
+  constexpr int n = U::n;
+  const int lane = threadIdx.x & 31;
+  const int u = threadIdx.x % U::kUnits;
+  const long long tok = static_cast<long long>(blockIdx.x) * (256 / U::kUnits) + threadIdx.x / U::kUnits;
+  const int t = static_cast<int>(tok < p.T ? tok : p.T);       // p.T: no token (cu_q[B] <= T)
+  const int b = find_sequence<U::kUnits>(p.cu_q, p.B, t, lane);
+  bool live = tok < p.T && b < p.B;
+  int pos = 0;
+  if (live) {
+    pos = p.kv_len[b] - p.cu_q[b + 1] + t;
+    live = pos >= 0;
+  }
+  const RopeUnit<T, D, INTER> unit(u, p.inv_freq ? p.rot : 0);
+  const int h0 = blockIdx.y * p.heads_per_block;
+  const int h1 = min(h0 + p.heads_per_block, p.Hq + 2 * p.c.Hkv);
+  // page and row of the token, needed for K and V heads only
+  long long slot = -1;          // page * page_size + row; -1: nowhere
+  if (live && h1 > p.Hq) {
+    const int pi = pos >> p.c.page_shift;
+    int page = -1;
+    if (pi < p.max_pages) page = p.table[static_cast<long long>(b) * p.max_pages + pi];
+    if (page >= 0 && page < p.c.num_pages)
+      slot = (static_cast<long long>(page) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));
+    else if (u == 0)
+      record_bad_page();
+  }
+  float cs[U::kPairs], sn[U::kPairs];
+  if (live && unit.turned) rope_sincos<U::kPairs>(p.inv_freq, unit.pair0, pos, p.mscale, 0, cs, sn);
+  for (int h = h0; h < h1; ++h) {
+    const bool isq = h < p.Hq, isk = !isq && h < p.Hq + p.c.Hkv;
+    const RowView& v = isq ? p.q : isk ? p.k : p.v;
+    const int hh = isq ? h : isk ? h - p.Hq : h - p.Hq - p.c.Hkv;
+    float a[n], bb[n];
+    uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+    if (live) {
+      const T* row = reinterpret_cast<const T*>(v.p) + t * v.st + hh * v.sh;
+      x0 = *reinterpret_cast<const uint4*>(row + unit.c0 * n);
+      if constexpr (U::NC == 2) x1 = *reinterpret_cast<const uint4*>(row + unit.c1 * n);
+    }
+    const bool turn = live && unit.turned && (isq || isk);
+    if (E4M3 || turn) {
+      Vec16<T>::load(x0, a);
+      if constexpr (U::NC == 2) Vec16<T>::load(x1, bb);
+    }
+    if (turn) rope_turn<T, INTER, U::kPairs, n>(a, bb, cs, sn);
+    if (isq || !E4M3) {
+      if (turn) {
+        x0 = Vec16<T>::store(a);
+        if constexpr (U::NC == 2) x1 = Vec16<T>::store(bb);
+      }
+      T* row = nullptr;
+      if (isq && live) {
+        row = reinterpret_cast<T*>(p.qo.p) + t * p.qo.st + hh * p.qo.sh;
+      } else if (!isq && slot >= 0) {
+        const long long page = slot >> p.c.page_shift;
+        const int r = static_cast<int>(slot & ((1 << p.c.page_shift) - 1));
+        row = reinterpret_cast<T*>((isk ? p.c.k : p.c.v) + page * p.c.page_bytes) +
+              ((static_cast<long long>(hh) << p.c.page_shift) + r) * D;
+      }
+      if (row) {
+        *reinterpret_cast<uint4*>(row + unit.c0 * n) = x0;
+        if constexpr (U::NC == 2) *reinterpret_cast<uint4*>(row + unit.c1 * n) = x1;
+      }
+    } else {
+      // the row's largest finite magnitude, over the lanes that share the row
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float m0 = fabsf(a[i]);
+        amax = fmaxf(amax, m0 < INFINITY ? m0 : 0.f);
+        if constexpr (U::NC == 2) {
+          const float m1 = fabsf(bb[i]);
+          amax = fmaxf(amax, m1 < INFINITY ? m1 : 0.f);
+        }
+      }
+#pragma unroll
+      for (int m = U::kUnits / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      const int e = e4m3_exponent(amax);
+      const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);      // 2^-e
+      auto codes = [&](const float (&x)[n]) {
+        return make_uint2(pack_e4m3x2(x[0] * f, x[1] * f) | (pack_e4m3x2(x[2] * f, x[3] * f) << 16),
+                          pack_e4m3x2(x[4] * f, x[5] * f) | (pack_e4m3x2(x[6] * f, x[7] * f) << 16));
+      };
+      if (slot >= 0) {
+        const long long page = slot >> p.c.page_shift;
+        const int r = static_cast<int>(slot & ((1 << p.c.page_shift) - 1));
+        const long long in_page = (static_cast<long long>(hh) << p.c.page_shift) + r;
+        char* row = (isk ? p.c.k : p.c.v) + page * p.c.page_bytes + in_page * D;
+        *reinterpret_cast<uint2*>(row + unit.c0 * n) = codes(a);
+        if constexpr (U::NC == 2) *reinterpret_cast<uint2*>(row + unit.c1 * n) = codes(bb);
+        if (u == 0)
+          (isk ? p.c.ks : p.c.vs)[((page * p.c.Hkv) << p.c.page_shift) + in_page] = static_cast<uint8_t>(e + 127);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ cache read
+struct ReadParams {
+  CacheView c;
+  __nv_bfloat16* ko;
+  __nv_bfloat16* vo;
+  const int* kv_len;
+  const int* table;
+  int max_pages, N;
+};
+
+// Four e4m3 codes times 2^(byte - 127), as two bf16x2 words, exact.  A code's exponent and
+// mantissa fields, shifted to where bf16 has its own, read as a bf16 of 2^-120 times the
+// code's value (subnormal codes too); the product with 2^(byte - 127 + 120) puts that
+// right.  lo and hi share that factor where it passes bf16's largest power.
+struct E4m3Scale {
+  __nv_bfloat162 lo, hi;
+  bool two;
+};
+__device__ __forceinline__ __nv_bfloat162 bf16x2_pow2(int e) {            // -133 <= e <= 127, as a pair
+  const uint32_t h = e >= -126 ? static_cast<uint32_t>(e + 127) << 7 : 1u << (e + 133);
+  const uint32_t w = h | (h << 16);
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+__device__ __forceinline__ E4m3Scale e4m3_scale(int byte) {
+  E4m3Scale s;
+  const int e = byte - 127 + 120;
+  s.two = e > 127;
+  s.lo = bf16x2_pow2(s.two ? 127 : e);
+  s.hi = bf16x2_pow2(s.two ? e - 127 : 0);
+  return s;
+}
+__device__ __forceinline__ uint32_t e4m3x2_widen(uint32_t x, const E4m3Scale& s) {
+  // x: two codes in the high bytes of its halves
+  const uint32_t w = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+  __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), s.lo);
+  if (s.two) v = __hmul2(v, s.hi);
+  // the two NaN codes (all ones) stay NaN
+  uint32_t r = *reinterpret_cast<uint32_t*>(&v);
+  if ((x & 0x7f000000u) == 0x7f000000u) r |= 0x7fc00000u;
+  if ((x & 0x00007f00u) == 0x00007f00u) r |= 0x00007fc0u;
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_widen(uint32_t codes, const E4m3Scale& s, uint32_t& w0, uint32_t& w1) {
+  w0 = e4m3x2_widen(__byte_perm(codes, 0, 0x1404), s);      // codes 0 and 1
+  w1 = e4m3x2_widen(__byte_perm(codes, 0, 0x3424), s);      // codes 2 and 3
+}
+
+// Grid: x over blocks of positions, y over (sequence, head).  A thread moves 16 output
+// bytes of K and of V at a position, ROWS positions per pass.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(256) attn_cache_read_kernel(const ReadParams p) {
+  constexpr int CPR = D / 8;                 // 16-byte output chunks per row
+  constexpr int RPB = 256 / CPR;             // rows per pass
+  constexpr int PASSES = 4;
+  const int bg = blockIdx.y, b = bg / p.c.Hkv, g = bg - b * p.c.Hkv;
+  const int len = min(p.kv_len[b], p.N);
+  const int first = blockIdx.x * (RPB * PASSES);
+  if (first >= len) return;
+  const int c = threadIdx.x % CPR;
+  uint4 kx[PASSES], vx[PASSES];
+  int pos[PASSES];
+  long long at[PASSES];                      // row in the pool, or -1
+  long long src[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    pos[i] = first + i * RPB + threadIdx.x / CPR;
+    at[i] = -1;
+    if (pos[i] < len) {
+      const int pi = pos[i] >> p.c.page_shift;
+      const int page = pi < p.max_pages ? p.table[static_cast<long long>(b) * p.max_pages + pi] : -1;
+      if (page >= 0 && page < p.c.num_pages) {
+        const long long in_page =
+            (static_cast<long long>(g) << p.c.page_shift) + (pos[i] & ((1 << p.c.page_shift) - 1));
+        at[i] = ((static_cast<long long>(page) * p.c.Hkv) << p.c.page_shift) + in_page;
+        src[i] = page * p.c.page_bytes + in_page * (E4M3 ? D : 2 * D);
+      } else if (c == 0) {
+        record_bad_page();
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (at[i] < 0) continue;
+    if constexpr (E4M3) {
+      const uint2 kc = *reinterpret_cast<const uint2*>(p.c.k + src[i] + c * 8);
+      const uint2 vc = *reinterpret_cast<const uint2*>(p.c.v + src[i] + c * 8);
+      const E4m3Scale ks = e4m3_scale(p.c.ks[at[i]]), vs = e4m3_scale(p.c.vs[at[i]]);
+      e4m3x4_widen(kc.x, ks, kx[i].x, kx[i].y);
+      e4m3x4_widen(kc.y, ks, kx[i].z, kx[i].w);
+      e4m3x4_widen(vc.x, vs, vx[i].x, vx[i].y);
+      e4m3x4_widen(vc.y, vs, vx[i].z, vx[i].w);
+    } else {
+      kx[i] = *reinterpret_cast<const uint4*>(p.c.k + src[i] + c * 16);
+      vx[i] = *reinterpret_cast<const uint4*>(p.c.v + src[i] + c * 16);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    if (pos[i] >= len) continue;
+    const long long o = (static_cast<long long>(bg) * p.N + pos[i]) * D + c * 8;
+    *reinterpret_cast<uint4*>(p.ko + o) = kx[i];
+    *reinterpret_cast<uint4*>(p.vo + o) = vx[i];
+  }
+}
+
+}  // namespace attn

@@ -1,0 +1,936 @@
+// Attention of new tokens over a paged K/V cache for sm_100a.
+//
+// Method (page "attn-efficient", online-softmax section; page "attention 的显存线性化",
+// reading list: FlashDecoding): the tiled online softmax of the forward, with K and V
+// tiles gathered from pages, and the keys of a query tile shared out over several CTAs
+// where there are few tiles.  With m = max_s LSE_s and w_s = exp(LSE_s - m) over the
+// shares s of a row: O = sum_s w_s O_s / sum_s w_s, LSE = m + ln sum_s w_s.
+//
+// Work.  An item is (sequence b, KV head g, block of R tokens): the G query heads of the
+// group times R = 128 / G tokens fill the 128 rows of a tensor-core tile (row = i * G + h),
+// so K and V of a group are read once for all its heads.  Its work is the number of
+// 128-key tiles that any of its rows sees.  All items' tiles, in the order (b, g, block),
+// form one line of W tiles, and CTA c takes the tiles [W c / C, W (c+1) / C): every SM
+// streams the same number of tiles whatever the lengths are.  Each CTA finds its place
+// from cu_q and kv_len alone (no plan from the host, no counter), so a captured launch
+// follows the lengths.  A CTA's share cuts at most two items; a cut item's parts go to
+// the workspace (two slots per CTA, independent of lengths) and the merge kernel joins
+// them in key order, so results do not depend on timing.
+#pragma once
+#include "bwd.cuh"     // bulk_load
+#include "cache.cuh"
+#include "fwd.cuh"
+
+namespace attn {
+
+struct PagedParams {
+  CacheView c;
+  __nv_bfloat16* o;           // [T][Hq][D]
+  float* lse;                 // [T][Hq]
+  const int* cu_q;
+  const int* kv_len;
+  const int* table;
+  int B, T, max_pages;
+  int Hq, Hkv, G, R;          // R tokens per tile, G * R <= 128
+  int RI;                     // tokens per item: R * teams
+  int causal, wl;             // wl < 0: no window
+  float cs;                   // scale * log2(e), floored (folded_scale)
+  int ctas;                   // CTAs of the launch
+  int min_tiles;              // no CTA's share is cut below this many tiles
+  int slot_rows;              // rows of a workspace slot
+  float* opart;               // [2 * ctas][slot_rows][D], normalised by the part's own sum
+  float* lpart;               // [2 * ctas][slot_rows], natural log; -inf: no key seen
+  struct PagedCut* cuts;      // [ctas]
+};
+
+// A cut item, written by the CTA that holds its first part.
+struct PagedCut {
+  int tok0, ntok, g;          // rows: tokens tok0 .. tok0 + ntok - 1 of KV head g; ntok = 0: nothing cut here
+  int parts;                  // part 0 in slot 2c + 1, part i in slot 2 (c + i)
+};
+
+// One piece of work of a CTA, posted to its consumer warps.
+struct PagedSeg {
+  int b, g;
+  int tok0, ntok;             // packed row of the first token, tokens of the item
+  int pos0;                   // position of the first token
+  int len;                    // keys of the sequence
+  int kmin;                   // first key that a row of the item sees
+  int j0, n;                  // key tiles [j0, j0 + n); n = 0 ends the sequence of pieces
+  int slot;                   // -1: write o and lse; else the workspace slot
+};
+
+// sum of floor(max(0, a + r i) / 128) over 0 <= i < x, for r >= 1, in a few steps: the
+// part of a and r that 128 divides is summed in closed form, the rest counts the lattice
+// points under a line, with the axes exchanged until nothing is left.
+__device__ __forceinline__ long long stair_sum(long long a, long long r, long long x) {
+  if (a < 0) {
+    const long long skip = (-a + r - 1) / r;
+    if (skip >= x) return 0;
+    a += r * skip;
+    x -= skip;
+  }
+  long long m = 128, sum = 0;
+  while (true) {
+    if (r >= m) { sum += x * (x - 1) / 2 * (r / m); r %= m; }
+    if (a >= m) { sum += x * (a / m); a %= m; }
+    const long long top = r * x + a;
+    if (top < m) return sum;
+    x = top / m;
+    a = top % m;
+    const long long t = m;
+    m = r;
+    r = t;
+  }
+}
+
+// The items of one (sequence, KV head).
+struct PagedSeq {
+  int nq, len, tok0;
+  int nblk;                   // items
+  __device__ __forceinline__ void load(const PagedParams& p, int b) {
+    tok0 = p.cu_q[b];
+    const int end = min(p.cu_q[b + 1], p.T);
+    nq = tok0 >= 0 ? max(0, end - tok0) : 0;
+    len = max(0, p.kv_len[b]);
+    // positions follow from the sequence's own count of tokens, also where T cuts it short
+    pos0 = len - max(nq, p.cu_q[b + 1] - tok0);
+    nblk = (nq + p.RI - 1) / p.RI;
+  }
+  int pos0;
+  // first and last key tile of item i
+  __device__ __forceinline__ void range(const PagedParams& p, int i, int& kmin, int& j0, int& n) const {
+    const int p0 = pos0 + i * p.RI, p1 = pos0 + min(nq, (i + 1) * p.RI) - 1;
+    kmin = p.wl >= 0 ? max(0, p0 - p.wl) : 0;
+    const int kmax = p.causal ? min(p1, len - 1) : len - 1;
+    j0 = kmin >> 7;
+    n = max(1, (max(kmax, 0) >> 7) - j0 + 1);
+  }
+  // key tiles of the items before item i
+  __device__ __forceinline__ long long before(const PagedParams& p, int i) const {
+    if (i <= 0) return 0;
+    long long last = 0;
+    if (i == nblk) {          // the last item may have fewer tokens
+      int kmin, j0, n;
+      range(p, i - 1, kmin, j0, n);
+      last = n;
+      if (--i == 0) return last;
+    }
+    const long long hi = p.causal ? stair_sum(pos0 + p.RI - 1, p.RI, i) : static_cast<long long>(max(len - 1, 0) >> 7) * i;
+    const long long lo = p.wl >= 0 ? stair_sum(static_cast<long long>(pos0) - p.wl, p.RI, i) : 0;
+    return last + hi - lo + i;
+  }
+  __device__ __forceinline__ long long tiles(const PagedParams& p) const { return before(p, nblk); }
+};
+
+// Where a CTA's share begins.
+struct PagedPlan {
+  long long warp_sum[32];
+  long long total;            // W
+  long long begin, end;       // this CTA's tiles
+  long long rest;             // begin, counted from the first tile of sequence b
+  long long head_tiles;       // tiles of one (b, g)
+  int parts;                  // C: CTAs that have a share
+  int b;
+};
+
+// Block-wide inclusive scan of v; returns this thread's prefix, total in all threads.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sum, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
+  __syncthreads();                            // warp_sum is free again
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int i = 0; i < nw; ++i) {
+    const long long s = warp_sum[i];
+    if (i < warp) before += s;
+    total += s;
+  }
+  return before + v;
+}
+
+// All threads of the CTA: W, the CTA's range and the sequence it begins in.
+__device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlan& pl, int cta) {
+  const int nt = blockDim.x;
+  long long mine = 0, incl = 0, total = 0, sum = 0;
+  for (int b0 = 0; b0 < p.B; b0 += nt) {
+    const int b = b0 + threadIdx.x;
+    mine = 0;
+    if (b < p.B) {
+      PagedSeq s;
+      s.load(p, b);
+      mine = s.tiles(p) * p.Hkv;
+    }
+    incl = block_scan(mine, pl.warp_sum, sum);
+    total += sum;
+  }
+  const long long most = total / p.min_tiles;
+  const int parts = static_cast<int>(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
+  const long long begin = cta < parts ? total * cta / parts : total, end = cta < parts ? total * (cta + 1) / parts : total;
+  if (threadIdx.x == 0) {
+    pl.total = total;
+    pl.parts = parts;
+    pl.begin = begin;
+    pl.end = end;
+    pl.b = p.B;
+  }
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += nt) {      // again, to find the sequence that holds tile `begin`
+    const int b = b0 + threadIdx.x;
+    if (p.B > nt) {
+      mine = 0;
+      if (b < p.B) {
+        PagedSeq s;
+        s.load(p, b);
+        mine = s.tiles(p) * p.Hkv;
+      }
+      incl = block_scan(mine, pl.warp_sum, sum);
+    }
+    const long long from = base + incl - mine;
+    if (b < p.B && begin < end && from <= begin && begin < from + mine) {
+      pl.b = b;
+      pl.rest = begin - from;
+      pl.head_tiles = mine / p.Hkv;
+    }
+    base += sum;
+  }
+  __syncthreads();
+}
+
+// The pieces of a CTA's share, in order.  Used by one whole warp (the first place needs
+// its lanes); afterwards every lane holds the same state.
+struct PagedWalk {
+  PagedSeq s;
+  int b, g, i;                // sequence, KV head, item
+  int skip;                   // tiles of the item that lie before the share
+  long long left;             // tiles still to hand out
+  __device__ __forceinline__ void begin(const PagedParams& p, const PagedPlan& pl, int lane) {
+    left = pl.end - pl.begin;
+    b = pl.b;
+    g = i = skip = 0;
+    if (left <= 0 || b >= p.B) { left = 0; return; }
+    s.load(p, b);
+    g = static_cast<int>(pl.rest / pl.head_tiles);
+    const long long rest = pl.rest - g * pl.head_tiles;
+    int lo = 0, hi = s.nblk;                  // before(lo) <= rest < before(hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = min(lo + (lane + 1) * step, hi);
+      const unsigned m = __ballot_sync(0xffffffffu, at < hi && s.before(p, at) <= rest);
+      lo += __popc(m) * step;
+      hi = min(lo + step, hi);
+    }
+    i = lo;
+    skip = static_cast<int>(rest - s.before(p, i));
+  }
+  // next piece; n = 0 when the share is used up
+  __device__ __forceinline__ PagedSeg next(const PagedParams& p, const PagedPlan& pl, int cta) {
+    PagedSeg w;
+    w.n = 0;
+    w.slot = -1;
+    if (left <= 0) return w;
+    while (i >= s.nblk) {                     // next head, next sequence that has tokens
+      i = 0;
+      if (++g >= p.Hkv || s.nblk == 0) {
+        g = 0;
+        if (++b >= p.B) { left = 0; return w; }
+        s.load(p, b);
+      }
+    }
+    int n;
+    s.range(p, i, w.kmin, w.j0, n);
+    w.b = b;
+    w.g = g;
+    w.tok0 = s.tok0 + i * p.RI;
+    w.ntok = min(p.RI, s.nq - i * p.RI);
+    w.pos0 = s.pos0 + i * p.RI;
+    w.len = s.len;
+    w.j0 += skip;
+    const int have = n - skip;
+    w.n = static_cast<int>(left < have ? left : have);
+    if (skip > 0) w.slot = 2 * cta;
+    else if (w.n < n) w.slot = 2 * cta + 1;
+    if (skip == 0 && w.n < n) {               // the first part of a cut item
+      const long long last = pl.end - left + n - 1;          // the item's last tile
+      const int c1 = static_cast<int>(((last + 1) * pl.parts - 1) / pl.total);
+      PagedCut& cut = p.cuts[cta];
+      cut.tok0 = w.tok0;
+      cut.ntok = w.ntok;
+      cut.g = g;
+      cut.parts = c1 - cta + 1;
+    }
+    left -= w.n;
+    skip = 0;
+    ++i;
+    return w;
+  }
+};
+
+// Pieces passed from the producer warp to the consumer warps, in order.
+struct SegRing {
+  uint64_t full[4];           // count 1
+  uint64_t empty[4];          // count = number of consumer warps
+  PagedSeg seg[4];
+};
+__device__ __forceinline__ void seg_ring_init(SegRing& r, uint32_t consumers) {
+  for (int i = 0; i < 4; ++i) {
+    mbar_init(&r.full[i], 1);
+    mbar_init(&r.empty[i], consumers);
+  }
+}
+// Producer (one thread): post the k-th piece; false if a wait failed.
+__device__ __forceinline__ bool seg_ring_post(SegRing& r, int k, const PagedSeg& w) {
+  const int i = k & 3;
+  if (k >= 4 && !mbar_wait(&r.empty[i], ((k >> 2) - 1) & 1)) return false;
+  r.seg[i] = w;
+  mbar_arrive(&r.full[i]);
+  return true;
+}
+// Consumer (whole warp): the k-th piece; n = 0 at the end or if a wait failed (ok = false).
+__device__ __forceinline__ PagedSeg seg_ring_take(SegRing& r, int k, int lane, bool& ok) {
+  const int i = k & 3;
+  PagedSeg w;
+  w.n = 0;
+  ok = __all_sync(0xffffffffu, mbar_wait(&r.full[i], (k >> 2) & 1));
+  if (!ok) return w;
+  w = r.seg[i];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&r.empty[i]);
+  return w;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* tmap, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// Programmatic dependent launch: wait until the kernels before this one have finished and
+// their writes are visible / let the next kernel's blocks start early.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ------------------------------------------------------------------ one query tile per CTA
+// Warps 0-7 softmax (two groups of 64 keys, thread = tile row = TMEM lane), warp 8
+// producer, warp 9 MMA issuer and, for an e4m3 cache, warps 10-17 that widen raw tiles to
+// bf16 ones.  TMEM: S in two buffers, so S of the next tile is computed while the softmax
+// works on this one, and O.
+template <int D, bool KV8>
+struct PagedCfg {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kBox = 128 * 128;
+  static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
+  static constexpr int QST = (KV8 && D == 128) ? 1 : 2;
+  static constexpr int KST = 2, VST = 2;
+  static constexpr int kWiden = KV8 ? 8 : 0;       // widening warps
+  static constexpr int kThreads = 320 + 32 * kWiden;
+  static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
+  static constexpr int RST = KV8 ? (D == 128 ? 3 : 6) : 0;   // raw stages, K and V tiles alternating
+  static constexpr int kRawStage = kRawTile + 128;           // codes, then scale bytes
+  static constexpr int kS0 = 0, kS1 = 128, kO = 256;
+  static constexpr int kTmemCols = 512;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = QST * kTile;
+  static constexpr int kOffV = kOffK + KST * kTile;
+  static constexpr int kOffRaw = kOffV + VST * kTile;
+  static constexpr int kOffSh = kOffRaw + ((RST * kRawStage + 127) / 128) * 128;
+  static constexpr int kLayout = kOffSh + 4608;
+  static constexpr int kSmem = kLayout + 1024;
+  static_assert(kSmem <= 232448, "shared memory layout exceeds 227 KB");
+};
+
+struct PagedShared {
+  float xmax[2][2][128];      // [step parity][group][row] partial row maxima
+  float xsum[2][128];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t raw_full[8], raw_empty[8];
+  uint64_t s_full[2], p_ready[2];
+  uint64_t pv_done;
+  uint64_t xbar[2][4];        // [step parity][quadrant]: both groups' warps posted their maxima
+  uint64_t sbar[4];
+  uint64_t o_free;
+  SegRing ring;
+  uint64_t drain, teardown;
+  PagedPlan plan;
+  uint32_t tmem_base;
+};
+static_assert(sizeof(PagedShared) <= 4608, "PagedShared does not fit its slot");
+
+// Key tile j of a piece, page by page: lane i of the producer warp brings in the i-th
+// (page, 64-column box) of the tile.
+struct PageTile {
+  int first, count;           // pages of the tile that hold keys in [kmin, len): local indices
+};
+__device__ __forceinline__ PageTile page_tile(const PagedParams& p, const PagedSeg& w, int j) {
+  const int lo = max(w.kmin, j * 128), hi = min(w.len, j * 128 + 128);
+  PageTile t;
+  t.first = 0;
+  t.count = 0;
+  if (hi <= lo) return t;
+  const int sh = p.c.page_shift < 7 ? p.c.page_shift : 7;      // pages larger than a tile count as one box
+  t.first = (lo - j * 128) >> sh;
+  t.count = ((hi - 1 - j * 128) >> sh) - t.first + 1;
+  return t;
+}
+
+// Page of local box x of tile j, or -1 (recorded) if the table does not lead into the pool.
+__device__ __forceinline__ int page_of(const PagedParams& p, const PagedSeg& w, int j, int x) {
+  const int sh = p.c.page_shift;
+  const int pi = sh <= 7 ? (j << (7 - sh)) + x : j >> (sh - 7);
+  int page = -1;
+  if (pi < p.max_pages) page = p.table[static_cast<long long>(w.b) * p.max_pages + pi];
+  if (page < 0 || page >= p.c.num_pages) {
+    record_bad_page();
+    page = -1;
+  }
+  return page;
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const PagedParams p) {
+  using C = PagedCfg<D, KV8>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PagedShared& sh = *reinterpret_cast<PagedShared*>(smem + C::kOffSh);
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+  uint8_t* sRaw = smem + C::kOffRaw;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.k_full[i], KV8 ? C::kWiden : 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], KV8 ? C::kWiden : 1);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], 8);
+      for (int q = 0; q < 4; ++q) mbar_init(&sh.xbar[i][q], 2);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], KV8 ? C::kWiden : 1);
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(&sh.sbar[q], 2);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.o_free, 8);
+    seg_ring_init(sh.ring, 9 + C::kWiden);
+    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.teardown, 10 + C::kWiden);
+    fence_barrier_init();
+  }
+  if (warp == 0) { tmem_alloc(&sh.tmem_base, C::kTmemCols); tmem_relinquish(); }
+  grid_dependency_wait();
+  grid_dependency_launch();
+  paged_plan(p, sh.plan, cta);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer (whole warp)
+    if (lane == 0) {
+      tma_prefetch_desc(&tmq); tma_prefetch_desc(&tmk); tma_prefetch_desc(&tmv);
+      p.cuts[cta].ntok = 0;
+    }
+    __syncwarp();
+    PagedWalk walk;
+    walk.begin(p, sh.plan, lane);
+    const int psh = p.c.page_shift < 7 ? p.c.page_shift : 7;
+    const int rows = 1 << psh;                      // rows of a box
+    int kc = 0, nk = 0, uq = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const PagedSeg w = walk.next(p, sh.plan, cta);
+      if (lane == 0) ok = seg_ring_post(sh.ring, k, w);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok || w.n == 0) break;
+      if (lane == 0) {
+        const int qs = uq % C::QST;
+        if (uq >= C::QST) ok = mbar_wait(&sh.q_empty[qs], ((uq / C::QST) - 1) & 1);
+        if (ok) {
+          mbar_arrive_expect_tx(&sh.q_full[qs], p.G * p.R * D * 2);
+          for (int c = 0; c < C::NB; ++c)
+            tma_load_3d(sQ + qs * C::kTile + c * C::kBox, &tmq, &sh.q_full[qs], c * 64, w.g * p.G, w.tok0);
+        }
+      }
+      ++uq;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      constexpr int NX = KV8 ? 1 : C::NB;           // column boxes per page
+      const int bx = lane / NX, bc = lane % NX;
+      int page = 0;
+      PageTile t = page_tile(p, w, w.j0);
+      if (ok && bx < t.count) page = page_of(p, w, w.j0, t.first + bx);
+      for (int j = 0; j < w.n && ok; ++j, ++kc) {
+        const int jt = w.j0 + j;
+        const PageTile tn = j + 1 < w.n ? page_tile(p, w, jt + 1) : PageTile{0, 0};
+        int page_n = 0;
+        if (bx < tn.count) page_n = page_of(p, w, jt + 1, tn.first + bx);     // in flight during this tile
+        const int y = p.c.page_shift > 7 ? (jt & ((1 << (p.c.page_shift - 7)) - 1)) * 128 : 0;
+        const int z = page < 0 ? p.c.num_pages : page;                        // outside the pool: zeros
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t *full, *empty;
+          uint8_t* dst;
+          int st, par;
+          bool wait;
+          if constexpr (KV8) {
+            const int rc = 2 * kc + kv;
+            st = rc % C::RST;
+            par = ((rc / C::RST) - 1) & 1;
+            wait = rc >= C::RST;
+            full = &sh.raw_full[st];
+            empty = &sh.raw_empty[st];
+            dst = sRaw + st * C::kRawStage;
+          } else {
+            st = kc & 1;
+            par = ((kc >> 1) - 1) & 1;
+            wait = kc >= 2;
+            full = kv ? &sh.v_full[st] : &sh.k_full[st];
+            empty = kv ? &sh.v_empty[st] : &sh.k_empty[st];
+            dst = (kv ? sV : sK) + st * C::kTile;
+          }
+          if (lane == 0) {
+            if (wait) ok = mbar_wait(empty, par);
+            if (ok) {
+              if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * (KV8 ? D + 1 : 2 * D));
+              else mbar_arrive(full);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (bx < t.count) {
+            const int r0 = (t.first + bx) << psh;    // row of the box in the tile
+            in_range(r0 + rows - 1, 128);
+            if constexpr (KV8) {
+              tma_load_4d(dst + r0 * D, kv ? &tmv : &tmk, full, 0, y, w.g, z);
+              const long long pg = page < 0 ? 0 : page;         // scale bytes of some page of the pool
+              bulk_load(dst + C::kRawTile + r0,
+                        (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y), rows, full);
+            } else {
+              tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? &tmv : &tmk, full, bc * 64, y, w.g, z);
+            }
+          }
+          nk = KV8 ? 2 * kc + kv + 1 : 2 * kc + kv + 1;
+        }
+        page = page_n;
+        t = tn;
+      }
+    }
+    if (!ok && lane == 0) {                          // let copies in flight land
+      if constexpr (KV8) {
+        for (int r = max(0, nk - C::RST); r < nk; ++r) mbar_drain_wait(&sh.raw_full[r % C::RST], (r / C::RST) & 1);
+      } else {
+        for (int r = max(0, nk - 4); r < nk; ++r)
+          mbar_drain_wait((r & 1) ? &sh.v_full[(r >> 1) & 1] : &sh.k_full[(r >> 1) & 1], (r >> 2) & 1);
+      }
+      for (int r = max(0, uq - C::QST); r < uq; ++r) mbar_drain_wait(&sh.q_full[r % C::QST], (r / C::QST) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    // Per piece: S(0), S(1); then per step j: PV(j), S(j + 2) into the buffer PV(j) just
+    // read (MMAs of one thread run in issue order, so PV(j) reads P(j) first).
+    const bool leader = elect_one();
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
+    constexpr uint32_t hi = sdesc_hi_sw128(1024);
+    const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
+    const uint32_t k_lo0 = sdesc_lo(smem_u32(sK), 16);
+    const uint32_t v_lo0 = sdesc_lo(smem_u32(sV), C::kBox);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    };
+    int kc = 0, vc = 0, gs = 0, uq = 0;
+    bool ok = true;
+    auto issue_s = [&](int g, int qs) -> bool {     // S(g) = Q K(kc)^T into buffer g % 2
+      const int st = kc & 1;
+      if (!wait(&sh.k_full[st], (kc >> 1) & 1)) return false;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t q_lo = q_lo0 + qs * (C::kTile >> 4);
+        const uint32_t k_lo = k_lo0 + st * (C::kTile >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::kBox + (k & 3) * 32) >> 4;
+          umma_ss_lo(tmem + ((g & 1) ? C::kS1 : C::kS0), q_lo + off, k_lo + off, hi, idS, k > 0);
+        }
+        umma_commit(&sh.s_full[g & 1]);
+        umma_commit(&sh.k_empty[st]);
+      }
+      __syncwarp();
+      ++kc;
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
+      if (w.n == 0) break;
+      const int qs = uq % C::QST;
+      ok = wait(&sh.q_full[qs], (uq / C::QST) & 1);
+      for (int t = 0; t < 2 && t < w.n && ok; ++t) {
+        ok = issue_s(gs + t, qs);
+        if (ok && t == w.n - 1 && leader) umma_commit(&sh.q_empty[qs]);
+        __syncwarp();
+      }
+      for (int j = 0; j < w.n && ok; ++j, ++vc) {
+        const int g = gs + j, vst = vc & 1;
+        ok = wait(&sh.v_full[vst], (vc >> 1) & 1);
+        if constexpr (!KV8) {
+          // Rows of V at keys that nobody sees (behind the sequence, before the window, in
+          // pages that were not loaded) are zeroed: their P is 0, and 0 times whatever lies
+          // there has to be 0.
+          const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
+          if (ok && (lo > 0 || hi_row < 128)) {
+            uint8_t* v = sV + vst * C::kTile;
+            for (int x = lane; x < 128 * 8; x += 32) {
+              const int r = x >> 3;
+              if (r >= lo && r < hi_row) continue;
+              for (int c = 0; c < C::NB; ++c)
+                *reinterpret_cast<uint4*>(v + c * C::kBox + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (ok) ok = wait(&sh.p_ready[g & 1], (g >> 1) & 1);
+        if (ok && j == 0 && uq >= 1) ok = wait(&sh.o_free, (uq - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t v_lo = v_lo0 + vst * (C::kTile >> 4);
+          const uint32_t sbase = tmem + ((g & 1) ? C::kS1 : C::kS0);
+#pragma unroll
+          for (int k2 = 0; k2 < 8; ++k2)
+            umma_ts_lo(tmem + C::kO, sbase + (k2 >> 2) * 64 + (k2 & 3) * 8, v_lo + ((k2 * 2048) >> 4), hi, idO,
+                       !(j == 0 && k2 == 0));
+          umma_commit(&sh.pv_done);
+          umma_commit(&sh.v_empty[vst]);
+        }
+        __syncwarp();
+        if (j + 2 < w.n) {
+          ok = issue_s(g + 2, qs);
+          if (ok && j + 2 == w.n - 1 && leader) umma_commit(&sh.q_empty[qs]);
+          __syncwarp();
+        }
+      }
+      gs += w.n;
+      ++uq;
+    }
+    if (leader) {
+      umma_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ widening warps (e4m3 cache)
+    // A lane takes 16 codes of a row, widens them with the row's scale and stores two
+    // 16-byte chunks of the bf16 tile in the 128B-swizzled layout the TMA would write.
+    if constexpr (KV8) {
+      const int wt = threadIdx.x - 320;             // 0 .. 32 * kWiden - 1
+      constexpr int CPR = D / 16;                   // 16-code chunks per row
+      constexpr int RPP = 32 * C::kWiden / CPR;     // rows per pass
+      const int c = wt % CPR;
+      int kc = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
+        if (w.n == 0) break;
+        for (int j = 0; j < w.n && ok; ++j, ++kc) {
+          const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
+          const int st = kc & 1;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int rc = 2 * kc + kv, rs = rc % C::RST;
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
+            if (ok && kc >= 2)
+              ok = __all_sync(0xffffffffu, mbar_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], ((kc >> 1) - 1) & 1));
+            if (!ok) break;
+            const uint8_t* raw = sRaw + rs * C::kRawStage;
+            uint8_t* out = (kv ? sV : sK) + st * C::kTile;
+#pragma unroll
+            for (int r0 = 0; r0 < 128; r0 += RPP) {
+              const int r = r0 + wt / CPR;
+              uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
+              const E4m3Scale s = e4m3_scale(raw[C::kRawTile + r]);
+              uint4 a, b;
+              e4m3x4_widen(x.x, s, a.x, a.y);
+              e4m3x4_widen(x.y, s, a.z, a.w);
+              e4m3x4_widen(x.z, s, b.x, b.y);
+              e4m3x4_widen(x.w, s, b.z, b.w);
+              if (kv && (r < lo || r >= hi_row)) a = b = make_uint4(0u, 0u, 0u, 0u);   // keys that nobody sees
+              // chunks 2c and 2c + 1 of the row, 8 to a 64-column box
+              const int box = c >> 2, cc = (2 * c) & 7;
+              uint8_t* row = out + box * C::kBox + r * 128;
+              *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = a;
+              *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = b;
+            }
+            fence_proxy_async_smem();               // generic-proxy writes -> tensor-core reads
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(kv ? &sh.v_full[st] : &sh.k_full[st]);
+              mbar_arrive(&sh.raw_empty[rs]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warps 0-7
+    const int grp = warp >> 2;                                  // keys [64 grp, 64 grp + 64)
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;                           // tile row = TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    constexpr int OH = D / 2;
+    const uint32_t o_base = lane_base + C::kO + grp * OH;
+    const float c = p.cs;
+    const uint64_t c2 = f2pack(c, c);
+    const int i = row / p.G, h = row - i * p.G;                 // token of the tile, head of the group
+    int gs = 0, uq = 0;
+    bool ok = true;
+    auto mask16 = [&](uint32_t (&r)[16], int col0, int lo, int lim) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (col0 + k < lo || col0 + k > lim) r[k] = 0xff800000u;
+    };
+    for (int k = 0; ok; ++k) {
+      const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
+      if (w.n == 0) break;
+      const bool valid = i < w.ntok && row < p.G * p.R;
+      const bool active = __any_sync(0xffffffffu, valid);       // a warp without rows only keeps step
+      const int pos = w.pos0 + i;
+      const int lastk = p.causal ? min(w.len - 1, pos) : w.len - 1;
+      const int firstk = p.wl >= 0 ? pos - p.wl : 0;
+      float m_used = -INFINITY;
+      uint64_t lsum = f2pack(0.f, 0.f);
+      for (int j = 0; j < w.n && ok; ++j) {
+        const int g2 = gs + j, xp = g2 & 1;
+        const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 64;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g2 & 1], (g2 >> 1) & 1));
+        if (!ok) break;
+        if (!active) {
+          if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
+          __syncwarp();
+          continue;
+        }
+        tc_fence_after();
+        const int kbase = (w.j0 + j) * 128 + grp * 64;
+        const int lo = firstk - kbase, lim = lastk - kbase;        // visible columns [lo, lim]
+        const bool msk = __any_sync(0xffffffffu, valid && (lo > 0 || lim < 63));
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+          uint32_t r0[16], r1[16], r2[16], r3[16];
+          tmem_ld16(s_base, r0);
+          tmem_ld16(s_base + 16, r1);
+          tmem_ld16(s_base + 32, r2);
+          tmem_ld16(s_base + 48, r3);
+          tmem_wait_ld();
+          reg_fence(r0);
+          reg_fence(r1);
+          reg_fence(r2);
+          reg_fence(r3);
+          if (msk) { mask16(r0, 0, lo, lim); mask16(r1, 16, lo, lim); mask16(r2, 32, lo, lim); mask16(r3, 48, lo, lim); }
+#pragma unroll
+          for (int kk = 0; kk < 16; kk += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              mx4[e] = max3f(mx4[e], __uint_as_float(r0[kk + e]), __uint_as_float(r0[kk + e + 4]));
+              mx4[e] = max3f(mx4[e], __uint_as_float(r1[kk + e]), __uint_as_float(r1[kk + e + 4]));
+              mx4[e] = max3f(mx4[e], __uint_as_float(r2[kk + e]), __uint_as_float(r2[kk + e + 4]));
+              mx4[e] = max3f(mx4[e], __uint_as_float(r3[kk + e]), __uint_as_float(r3[kk + e + 4]));
+            }
+          }
+        }
+        sh.xmax[xp][grp][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.xbar[xp][quad]);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[xp][quad], (g2 >> 1) & 1));
+        if (!ok) break;
+        const float mx = fmaxf(sh.xmax[xp][0][row], sh.xmax[xp][1][row]);
+        const float m_tile = mx == -INFINITY ? -INFINITY : mx * c;
+        float alpha = 1.f;
+        // a row that has seen no key keeps m_used = -inf (and p = 0) until it sees one
+        const bool need = valid && m_tile > m_used + kRescaleTau;
+        if (need) {
+          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx(m_used - m_tile);
+          float l0, l1;
+          f2unpack(lsum, l0, l1);
+          lsum = f2pack(l0 * alpha, l1 * alpha);
+          m_used = m_tile;
+        }
+        // S(j) was issued before PV(j - 1) (and after PV(j - 2), which its commit covers):
+        // wait for PV(j - 1) before rescaling O
+        if (__any_sync(0xffffffffu, need && j > 0)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, (g2 - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q4 = 0; q4 < OH / 16; ++q4) {
+            uint32_t o[16];
+            tmem_ld16(o_base + q4 * 16, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk)
+              o[kk] = alpha == 0.f ? 0u : __float_as_uint(__uint_as_float(o[kk]) * alpha);
+            tmem_st16(o_base + q4 * 16, o);
+          }
+        }
+        const float mb = m_used == -INFINITY ? 0.f : m_used;
+        const uint64_t nm2 = f2pack(-mb, -mb);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t r[16];
+          tmem_ld16(s_base + cc * 16, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          if (msk) mask16(r, cc * 16, lo, lim);
+          uint32_t pk[8];
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t xx =
+                ffma2(f2pack(__uint_as_float(r[2 * kk]), __uint_as_float(r[2 * kk + 1])), c2, nm2);
+            float x0, x1;
+            f2unpack(xx, x0, x1);
+            const float a0 = ex2_approx(x0), a1 = ex2_approx(x1);
+            lsum = fadd2(lsum, f2pack(a0, a1));
+            pk[kk] = pack_bf16x2(a0, a1);
+          }
+          tmem_st8(s_base + cc * 8, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
+      }
+      if (!ok) break;
+      // epilogue: the two groups' sums, the last PV, O / l and the LSE of this piece
+      const int glast = gs + w.n - 1;
+      float l = 0.f;
+      if (active) {
+        float l0, l1;
+        f2unpack(lsum, l0, l1);
+        sh.xsum[grp][row] = l0 + l1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.sbar[quad]);
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar[quad], uq & 1));
+      if (!ok) break;
+      if (active) l = sh.xsum[0][row] + sh.xsum[1][row];
+      // pv_done completes once per step.  S(glast) covered PV(glast - 2) only, so the
+      // phases of PV(glast - 1) and PV(glast) are waited for in turn (a parity wait
+      // can only tell apart the phase in progress and the one before it).
+      if (glast >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, (glast - 1) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, glast & 1));
+      if (!ok) break;
+      if (active) {
+        tc_fence_after();
+        const bool none = l == 0.f;                               // no key seen
+        const float inv_l = none ? 0.f : 1.f / l;
+        const float lse_s = none ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
+        const size_t orow = static_cast<size_t>(w.tok0 + i) * p.Hq + w.g * p.G + h;
+        const bool store = valid && in_range(w.tok0 + i, p.T) && in_range(row, w.slot < 0 ? 128 : p.slot_rows);
+#pragma unroll 1
+        for (int q4 = 0; q4 < OH / 16; ++q4) {
+          uint32_t o[16];
+          tmem_ld16(o_base + q4 * 16, o);
+          tmem_wait_ld();
+          reg_fence(o);
+          if (!store) continue;
+          float f[16];
+#pragma unroll
+          for (int kk = 0; kk < 16; ++kk) f[kk] = none ? 0.f : __uint_as_float(o[kk]) * inv_l;
+          if (w.slot < 0) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) pk[kk] = pack_bf16x2(f[2 * kk], f[2 * kk + 1]);
+            uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + grp * OH + q4 * 16);
+            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(
+                p.opart + (static_cast<size_t>(w.slot) * p.slot_rows + row) * D + grp * OH + q4 * 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              dst[kk] = make_float4(f[4 * kk], f[4 * kk + 1], f[4 * kk + 2], f[4 * kk + 3]);
+          }
+        }
+        if (store && grp == 0) {
+          if (w.slot < 0) p.lse[orow] = lse_s;
+          else p.lpart[static_cast<size_t>(w.slot) * p.slot_rows + row] = lse_s;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.o_free);
+      gs += w.n;
+      ++uq;
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.teardown);
+  if (warp == 0) {
+    mbar_wait(&sh.teardown, 0);
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Merge of cut items: block x looks after the item whose first part CTA x holds, the
+// blocks along y share its rows; one warp per row, D / 32 columns per lane.
+template <int D>
+__global__ void __launch_bounds__(128) attn_paged_merge_kernel(const PagedParams p) {
+  grid_dependency_wait();
+  constexpr int PER = D / 32;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const PagedCut cut = p.cuts[c];
+  const int rows = cut.ntok * p.G;
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
+    auto at = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.slot_rows + r; };
+    float m = -INFINITY;
+    for (int s = lane; s < cut.parts; s += 32) m = fmaxf(m, p.lpart[at(s)]);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float acc[PER];
+#pragma unroll
+    for (int x = 0; x < PER; ++x) acc[x] = 0.f;
+    float wsum = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < cut.parts; ++s) {
+      const float ls = p.lpart[at(s)];
+      const float w = ls == -INFINITY ? 0.f : ex2_approx((ls - m) * 1.4426950408889634f);
+      wsum += w;
+      const float* src = p.opart + at(s) * D + lane * PER;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) acc[x] = fmaf(w, src[x], acc[x]);
+    }
+    const int i = r / p.G, h = r - i * p.G;
+    const size_t orow = static_cast<size_t>(cut.tok0 + i) * p.Hq + cut.g * p.G + h;
+    const bool none = wsum == 0.f;
+    const float inv = none ? 0.f : 1.f / wsum;
+    __nv_bfloat16* dst = p.o + orow * D + lane * PER;
+#pragma unroll
+    for (int x = 0; x < PER; x += 2)
+      *reinterpret_cast<uint32_t*>(dst + x) = pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
+    if (lane == 0) p.lse[orow] = none ? -INFINITY : m + __logf(wsum);
+  }
+}
+
+}  // namespace attn

@@ -1,0 +1,406 @@
+// Host side of include/attn_paged.h: validation, tensor maps and launches of the serving
+// operators.  Included by api.cu, whose device query, alignment test and encoder it uses.
+#pragma once
+#include "attn_paged.h"
+#include "paged.cuh"
+
+namespace {
+
+bool stride_ok(const attn_strides_t* s, int elem, bool batch) {
+  auto ok = [&](long long x) { return x >= 0 && (x * elem) % 16 == 0 && x < (1ll << 38); };
+  return s && ok(s->head) && ok(s->token) && (!batch || ok(s->batch));
+}
+
+attn::RowView row_view(const void* p, const attn_strides_t* s) {
+  return {static_cast<char*>(const_cast<void*>(p)), s ? s->batch : 0, s ? s->head : 0, s ? s->token : 0};
+}
+
+int check_rope(const attn_rope_t* r, int d) {
+  if (!r->inv_freq || r->rot < 16 || r->rot > d || r->rot % 16 != 0) return ATTN_ERR_INVALID_ARG;
+  if ((r->interleaved != 0 && r->interleaved != 1) || !std::isfinite(r->mscale)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(r->inv_freq)) return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
+
+int check_cache(const attn_cache_t* c) {
+  if (!c) return ATTN_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (c->dtype != ATTN_BF16 && c->dtype != ATTN_E4M3) return ATTN_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return ATTN_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->Hkv < 1 || c->Hkv > 65535) return ATTN_ERR_INVALID_ARG;
+  const long long page = static_cast<long long>(c->Hkv) * c->page_size * c->d;
+  const int elem = c->dtype == ATTN_BF16 ? 2 : 1;
+  if (c->page_stride < page || c->page_stride >= (1ll << 38) || (c->page_stride * elem) % 16 != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!c->k || !c->v || (c->dtype == ATTN_E4M3 && (!c->k_scale || !c->v_scale))) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return ATTN_ERR_ALIGNMENT;
+  if (c->dtype == ATTN_E4M3 && (!aligned16(c->k_scale) || !aligned16(c->v_scale))) return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
+
+// int32 arrays: any 4-byte alignment will do (they are read word by word)
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_batch(const attn_batch_t* b, bool packed) {
+  if (!b || b->B < 1 || b->max_pages < 1 || !b->kv_len || !b->block_table) return ATTN_ERR_INVALID_ARG;
+  if (packed && (b->T < 0 || !b->cu_q)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(b->kv_len) || !aligned4(b->block_table) || (packed && !aligned4(b->cu_q))) return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
+
+attn::CacheView cache_view(const attn_cache_t* c) {
+  attn::CacheView v;
+  v.k = static_cast<char*>(c->k);
+  v.v = static_cast<char*>(c->v);
+  v.ks = static_cast<uint8_t*>(c->k_scale);
+  v.vs = static_cast<uint8_t*>(c->v_scale);
+  v.page_bytes = c->page_stride * (c->dtype == ATTN_BF16 ? 2 : 1);
+  v.num_pages = c->num_pages;
+  v.page_shift = 0;
+  while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
+  v.Hkv = c->Hkv;
+  return v;
+}
+
+// Heads that one block walks through: all of them where the tokens alone fill the GPU
+// (sine and cosine are then formed once per token), else few enough that the blocks do.
+int heads_per_block(long long token_blocks, int heads, int sms) {
+  const long long want = 8LL * sms;                       // blocks of 256 threads
+  long long split = (want + token_blocks - 1) / token_blocks;
+  if (split > heads) split = heads;
+  return static_cast<int>((heads + split - 1) / split);
+}
+
+template <typename T, int D, bool INTER>
+void launch_rope(const attn::RopeParams& p0, int sms, cudaStream_t s) {
+  attn::RopeParams p = p0;
+  constexpr int tpb = 256 / attn::RopeUnit<T, D, INTER>::kUnits;
+  const long long tb = (static_cast<long long>(p.B) * p.N + tpb - 1) / tpb;
+  p.heads_per_block = heads_per_block(tb, p.Hq + p.Hk, sms);
+  const dim3 grid(static_cast<unsigned>(tb), (p.Hq + p.Hk + p.heads_per_block - 1) / p.heads_per_block);
+  attn::attn_rope_kernel<T, D, INTER><<<grid, 256, 0, s>>>(p);
+}
+
+template <int D, bool E4M3, bool INTER>
+void launch_cache_write(const attn::WriteParams& p0, int sms, cudaStream_t s) {
+  attn::WriteParams p = p0;
+  constexpr int tpb = 256 / attn::RopeUnit<__nv_bfloat16, D, INTER>::kUnits;
+  const long long tb = (static_cast<long long>(p.T) + tpb - 1) / tpb;
+  const int heads = p.Hq + 2 * p.c.Hkv;
+  p.heads_per_block = heads_per_block(tb, heads, sms);
+  const dim3 grid(static_cast<unsigned>(tb), (heads + p.heads_per_block - 1) / p.heads_per_block);
+  attn::attn_cache_write_kernel<D, E4M3, INTER><<<grid, 256, 0, s>>>(p);
+}
+
+template <int D, bool E4M3>
+void launch_cache_read(const attn::ReadParams& p, int B, cudaStream_t s) {
+  constexpr int rows = 256 / (D / 8) * 4;
+  const dim3 grid((p.N + rows - 1) / rows, static_cast<unsigned>(B * p.c.Hkv));
+  attn::attn_cache_read_kernel<D, E4M3><<<grid, 256, 0, s>>>(p);
+}
+
+// [num_pages][Hkv][page_size][d] as a 4-D map; one box is a page's (or 128 rows of it)
+// 64 bf16 columns, swizzled as the MMAs read them, or all e4m3 columns as they lie.
+bool make_cache_map(CUtensorMap* m, const void* ptr, const attn_cache_t* c) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const int elem = c->dtype == ATTN_BF16 ? 2 : 1;
+  const cuuint64_t row = static_cast<cuuint64_t>(c->d) * elem;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page_size),
+                        static_cast<cuuint64_t>(c->Hkv), static_cast<cuuint64_t>(c->num_pages)};
+  cuuint64_t strides[3] = {row, row * c->page_size, static_cast<cuuint64_t>(c->page_stride) * elem};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(elem == 2 ? 64 : c->d),
+                       static_cast<cuuint32_t>(c->page_size < 128 ? c->page_size : 128), 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+             const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             elem == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [T][Hq][d] as a 3-D map; a box is 64 columns of G heads of R tokens: rows i * G + h of a tile.
+bool make_q_map(CUtensorMap* m, const void* q, const attn_strides_t* st, int T, int Hq, int d, int G, int R) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T)};
+  // a stride that no element uses (one head, one token) may be anything: give a plain one
+  const long long head = Hq > 1 ? st->head : d, token = T > 1 ? st->token : static_cast<long long>(Hq) * d;
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(token) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(R)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch with programmatic stream serialisation: the kernel may be set up while the one
+// before it runs, and waits for it on the device (griddepcontrol.wait).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Workspace of the cut items: descriptors, LSE of the parts, then their O (fp32).
+struct PagedWs {
+  int slot_rows;
+  size_t l_off, o_off, total;
+};
+PagedWs paged_ws(int T, int G, int d, int sms) {
+  PagedWs w;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const long long R = 128 / G;
+  w.slot_rows = static_cast<int>((T < R ? T : R) * G);
+  w.l_off = up(sizeof(attn::PagedCut) * sms);
+  w.o_off = up(w.l_off + static_cast<size_t>(2) * sms * w.slot_rows * 4);
+  w.total = up(w.o_off + static_cast<size_t>(2) * sms * w.slot_rows * d * 4);
+  return w;
+}
+
+int check_paged_heads(int T, int B, int Hq, int Hkv, int d) {
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * Hq >= (1ll << 38)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+template <int D, bool KV8>
+int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const attn::PagedParams& p,
+                 int merge_rows, cudaStream_t stream) {
+  using C = attn::PagedCfg<D, KV8>;
+  static std::once_flag attr_once[64];
+  static bool attr_ok[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::call_once(attr_once[dev], [&] {
+    attr_ok[dev] = cudaFuncSetAttribute(attn::attn_paged_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::kSmem) == cudaSuccess;
+  });
+  if (!attr_ok[dev]) return ATTN_ERR_LAUNCH;
+  if (launch_pdl(attn::attn_paged_kernel<D, KV8>, dim3(p.ctas), C::kThreads, C::kSmem, stream, tq, tk, tv, p) !=
+      cudaSuccess)
+    return ATTN_ERR_LAUNCH;
+  const dim3 grid(p.ctas, (merge_rows + 15) / 16);
+  if (launch_pdl(attn::attn_paged_merge_kernel<D>, grid, 128, 0, stream, p) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope(const void* q, const attn_strides_t* q_strides, void* q_out, const attn_strides_t* q_out_strides, int Hq,
+              const void* k, const attn_strides_t* k_strides, void* k_out, const attn_strides_t* k_out_strides, int Hkv,
+              int dtype, int B, int N, int d, const int* positions, long long pos_batch_stride,
+              const attn_rope_t* rope, int inverse, void* stream) {
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (dtype != ATTN_BF16 && dtype != ATTN_F32) return ATTN_ERR_INVALID_ARG;
+  if (!rope || Hq < 1 || B < 0 || N < 0 || (k && Hkv < 1)) return ATTN_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return ATTN_ERR_INVALID_ARG;
+  if (pos_batch_stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  const int elem = dtype == ATTN_BF16 ? 2 : 4;
+  if (!stride_ok(q_strides, elem, true) || !stride_ok(q_out_strides, elem, true)) return ATTN_ERR_INVALID_ARG;
+  if (k && (!stride_ok(k_strides, elem, true) || !stride_ok(k_out_strides, elem, true))) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(Hq) + (k ? Hkv : 0) > 65535) return ATTN_ERR_INVALID_ARG;
+  const int st = check_rope(rope, d);
+  if (st != ATTN_OK) return st;
+  if (B == 0 || N == 0) return ATTN_OK;
+  if (!q || !q_out || !positions || (k && !k_out)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || (k && (!aligned16(k) || !aligned16(k_out))) || !aligned4(positions))
+    return ATTN_ERR_ALIGNMENT;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
+  attn::RopeParams p;
+  p.q = row_view(q, q_strides);
+  p.qo = row_view(q_out, q_out_strides);
+  p.k = row_view(k, k ? k_strides : nullptr);
+  p.ko = row_view(k ? k_out : nullptr, k ? k_out_strides : nullptr);
+  p.Hq = Hq;
+  p.Hk = k ? Hkv : 0;
+  p.B = B;
+  p.N = N;
+  p.pos = positions;
+  p.pos_sb = pos_batch_stride;
+  p.inv_freq = rope->inv_freq;
+  p.rot = rope->rot;
+  p.inverse = inverse;
+  p.mscale = rope->mscale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto tag, auto dim) {
+    using T = decltype(tag);
+    constexpr int D = decltype(dim)::value;
+    if (rope->interleaved) launch_rope<T, D, true>(p, di->sms, s);
+    else launch_rope<T, D, false>(p, di->sms, s);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == ATTN_BF16) {
+    if (d == 64) go(__nv_bfloat16(), D64()); else go(__nv_bfloat16(), D128());
+  } else {
+    if (d == 64) go(0.f, D64()); else go(0.f, D128());
+  }
+  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_cache_write(const attn_cache_t* cache, const attn_batch_t* batch, const void* k,
+                     const attn_strides_t* k_strides, const void* v, const attn_strides_t* v_strides,
+                     const attn_rope_t* rope, const void* q, const attn_strides_t* q_strides, void* q_out,
+                     const attn_strides_t* q_out_strides, int Hq, void* stream) {
+  int st = check_cache(cache);
+  if (st == ATTN_OK) st = check_batch(batch, true);
+  if (st == ATTN_OK && rope) st = check_rope(rope, cache->d);
+  if (st != ATTN_OK) return st;
+  if (batch->T == 0) return ATTN_OK;
+  if (!k || !v || !stride_ok(k_strides, 2, false) || !stride_ok(v_strides, 2, false)) return ATTN_ERR_INVALID_ARG;
+  if (q && (!rope || !q_out || Hq < 1 || !stride_ok(q_strides, 2, false) || !stride_ok(q_out_strides, 2, false)))
+    return ATTN_ERR_INVALID_ARG;
+  const long long heads = (q ? static_cast<long long>(Hq) : 0) + 2LL * cache->Hkv;
+  if (heads > 65535) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out)))) return ATTN_ERR_ALIGNMENT;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
+  attn::WriteParams p;
+  p.c = cache_view(cache);
+  p.k = row_view(k, k_strides);
+  p.v = row_view(v, v_strides);
+  p.q = row_view(q, q ? q_strides : nullptr);
+  p.qo = row_view(q ? q_out : nullptr, q ? q_out_strides : nullptr);
+  p.Hq = q ? Hq : 0;
+  p.cu_q = batch->cu_q;
+  p.kv_len = batch->kv_len;
+  p.table = batch->block_table;
+  p.B = batch->B;
+  p.T = batch->T;
+  p.max_pages = batch->max_pages;
+  p.inv_freq = rope ? rope->inv_freq : nullptr;
+  p.rot = rope ? rope->rot : 0;
+  p.mscale = rope ? rope->mscale : 1.f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool inter = rope && rope->interleaved, e4m3 = cache->dtype == ATTN_E4M3;
+  auto go = [&](auto dim, auto eight) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool E = decltype(eight)::value;
+    if (inter) launch_cache_write<D, E, true>(p, di->sms, s);
+    else launch_cache_write<D, E, false>(p, di->sms, s);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (cache->d == 64) {
+    if (e4m3) go(D64(), std::true_type()); else go(D64(), std::false_type());
+  } else {
+    if (e4m3) go(D128(), std::true_type()); else go(D128(), std::false_type());
+  }
+  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* k_out, void* v_out, int N,
+                    void* stream) {
+  int st = check_cache(cache);
+  if (st == ATTN_OK) st = check_batch(batch, false);
+  if (st != ATTN_OK) return st;
+  if (N < 0) return ATTN_ERR_INVALID_ARG;
+  if (N == 0) return ATTN_OK;
+  if (!k_out || !v_out) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(batch->B) * cache->Hkv > 65535) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return ATTN_ERR_ALIGNMENT;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
+  attn::ReadParams p;
+  p.c = cache_view(cache);
+  p.ko = static_cast<__nv_bfloat16*>(k_out);
+  p.vo = static_cast<__nv_bfloat16*>(v_out);
+  p.kv_len = batch->kv_len;
+  p.table = batch->block_table;
+  p.max_pages = batch->max_pages;
+  p.N = N;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->dtype == ATTN_E4M3;
+  if (cache->d == 64) {
+    if (e4m3) launch_cache_read<64, true>(p, batch->B, s); else launch_cache_read<64, false>(p, batch->B, s);
+  } else {
+    if (e4m3) launch_cache_read<128, true>(p, batch->B, s); else launch_cache_read<128, false>(p, batch->B, s);
+  }
+  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+size_t attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d) {
+  if (check_paged_heads(T, B, Hq, Hkv, d) != ATTN_OK || T == 0) return 0;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != 0) return 0;
+  return paged_ws(T, Hq / Hkv, d, di->sms).total;
+}
+
+int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache, const attn_batch_t* batch,
+               void* o, float* lse, int Hq, float scale, int causal, int window_left, void* workspace,
+               size_t workspace_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st == ATTN_OK) st = check_batch(batch, true);
+  if (st == ATTN_OK) st = check_paged_heads(batch->T, batch->B, Hq, cache->Hkv, cache->d);
+  if (st != ATTN_OK) return st;
+  if (!std::isfinite(scale) || scale < 0.f || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (batch->T == 0) return ATTN_OK;
+  if (!q || !o || !lse || !stride_ok(q_strides, 2, false)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_ALIGNMENT;
+  if (workspace && !aligned16(workspace)) return ATTN_ERR_ALIGNMENT;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
+  const int d = cache->d, G = Hq / cache->Hkv;
+  const PagedWs W = paged_ws(batch->T, G, d, di->sms);
+  if (workspace && workspace_bytes < W.total) return ATTN_ERR_WORKSPACE;
+  CUtensorMap tq, tk, tv;
+  if (!make_q_map(&tq, q, q_strides, batch->T, Hq, d, G, 128 / G) || !make_cache_map(&tk, cache->k, cache) ||
+      !make_cache_map(&tv, cache->v, cache))
+    return ATTN_ERR_LAUNCH;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ws = workspace;
+  if (!ws && cudaMallocAsync(&ws, W.total, s) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return ATTN_ERR_ALLOC;
+  }
+  attn::PagedParams p;
+  p.c = cache_view(cache);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.cu_q = batch->cu_q;
+  p.kv_len = batch->kv_len;
+  p.table = batch->block_table;
+  p.B = batch->B;
+  p.T = batch->T;
+  p.max_pages = batch->max_pages;
+  p.Hq = Hq;
+  p.Hkv = cache->Hkv;
+  p.G = G;
+  p.R = 128 / G;
+  p.RI = p.R;
+  p.causal = causal;
+  p.wl = window_left < 0 ? -1 : window_left;
+  p.cs = attn::folded_scale(scale);
+  p.ctas = di->sms;
+  p.min_tiles = 1;
+  p.slot_rows = W.slot_rows;
+  p.cuts = static_cast<attn::PagedCut*>(ws);
+  p.lpart = reinterpret_cast<float*>(static_cast<char*>(ws) + W.l_off);
+  p.opart = reinterpret_cast<float*>(static_cast<char*>(ws) + W.o_off);
+  int st2;
+  if (cache->dtype == ATTN_E4M3)
+    st2 = d == 64 ? launch_paged<64, true>(tq, tk, tv, p, W.slot_rows, s) : launch_paged<128, true>(tq, tk, tv, p, W.slot_rows, s);
+  else
+    st2 = d == 64 ? launch_paged<64, false>(tq, tk, tv, p, W.slot_rows, s) : launch_paged<128, false>(tq, tk, tv, p, W.slot_rows, s);
+  if (!workspace && cudaFreeAsync(ws, s) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return st2 != ATTN_OK ? st2 : ATTN_ERR_ALLOC;
+  }
+  return st2;
+}
+
+}  // extern "C"
