@@ -348,14 +348,14 @@ struct PagedCfg {
 };
 
 struct PagedShared {
-  float xmax[2][2][128];      // [step parity][group][row] partial row maxima
+  float xmax[2][2][128];      // [parity of the quadrant's steps][group][row] partial row maxima
   float xsum[2][128];
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[8], raw_empty[8];
   uint64_t s_full[2], p_ready[2];
-  uint64_t pv_done;
-  uint64_t xbar[2][4];        // [step parity][quadrant]: both groups' warps posted their maxima
+  uint64_t pv_done[2];        // P V of step g complete, by g % 2: a waiter may be a step behind
+  uint64_t xbar[2][4];        // [parity][quadrant]: both groups' warps posted their maxima
   uint64_t sbar[4];
   uint64_t o_free;
   SegRing ring;
@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_ready[i], 8);
+      mbar_init(&sh.pv_done[i], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&sh.xbar[i][q], 2);
     }
     for (int i = 0; i < 8; ++i) {
@@ -427,7 +428,6 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
       mbar_init(&sh.raw_empty[i], KV8 ? C::kWiden : 1);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&sh.sbar[q], 2);
-    mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.o_free, 8);
     seg_ring_init(sh.ring, 9 + C::kWiden);
     mbar_init(&sh.drain, 1);
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
           for (int k2 = 0; k2 < 8; ++k2)
             umma_ts_lo(tmem + C::kO, sbase + (k2 >> 2) * 64 + (k2 & 3) * 8, v_lo + ((k2 * 2048) >> 4), hi, idO,
                        !(j == 0 && k2 == 0));
-          umma_commit(&sh.pv_done);
+          umma_commit(&sh.pv_done[g & 1]);
           umma_commit(&sh.v_empty[vst]);
         }
         __syncwarp();
@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
     const uint64_t c2 = f2pack(c, c);
     const int i = row / p.G, h = row - i * p.G;                 // token of the tile, head of the group
     int gs = 0, uq = 0;
+    int xs = 0;                 // steps in which this quadrant had rows: its maxima barriers' count
     bool ok = true;
     auto mask16 = [&](uint32_t (&r)[16], int col0, int lo, int lim) {
 #pragma unroll
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
       float m_used = -INFINITY;
       uint64_t lsum = f2pack(0.f, 0.f);
       for (int j = 0; j < w.n && ok; ++j) {
-        const int g2 = gs + j, xp = g2 & 1;
+        const int g2 = gs + j, xp = xs & 1;
         const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 64;
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g2 & 1], (g2 >> 1) & 1));
         if (!ok) break;
@@ -759,8 +760,9 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
         sh.xmax[xp][grp][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.xbar[xp][quad]);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[xp][quad], (g2 >> 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[xp][quad], (xs >> 1) & 1));
         if (!ok) break;
+        ++xs;
         const float mx = fmaxf(sh.xmax[xp][0][row], sh.xmax[xp][1][row]);
         const float m_tile = mx == -INFINITY ? -INFINITY : mx * c;
         float alpha = 1.f;
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
         // S(j) was issued before PV(j - 1) (and after PV(j - 2), which its commit covers):
         // wait for PV(j - 1) before rescaling O
         if (__any_sync(0xffffffffu, need && j > 0)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, (g2 - 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g2 - 1) & 1], ((g2 - 1) >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -832,11 +834,9 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar[quad], uq & 1));
       if (!ok) break;
       if (active) l = sh.xsum[0][row] + sh.xsum[1][row];
-      // pv_done completes once per step.  S(glast) covered PV(glast - 2) only, so the
-      // phases of PV(glast - 1) and PV(glast) are waited for in turn (a parity wait
-      // can only tell apart the phase in progress and the one before it).
-      if (glast >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, (glast - 1) & 1));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, glast & 1));
+      // PV(glast): S(glast) covered PV(glast - 2), the one before it on this barrier, so the
+      // parity is unambiguous (a parity wait tells apart two successive phases only)
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
       if (!ok) break;
       if (active) {
         tc_fence_after();

@@ -394,6 +394,22 @@ def test_paged_attention_matches_the_definition(attn, case, checks):
     check_attention(*run_paged(attn, case, seed=sum(case[5]) + case[2], checks=checks))
 
 
+def ragged(B, seed):
+    """Ragged batch whose tiles outnumber the SMs several times, so that every CTA works on several
+    items of very different row counts, one after the other."""
+    g = torch.Generator().manual_seed(seed)
+    new = [int(n) for n in torch.randint(0, 90, (B,), generator=g)]
+    new[1::3] = [1] * len(new[1::3])
+    return new, [n + int(x) for n, x in zip(new, torch.randint(0, 700, (B,), generator=g))]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page,e4m3,window", [(8, 8, 64, 16, False, None), (12, 4, 128, 64, False, 200),
+                                                       (16, 16, 128, 32, True, None), (20, 4, 64, 128, True, 77)])
+def test_paged_attention_of_many_ragged_items(attn, Hq, Hkv, d, page, e4m3, window):
+    new, lens = ragged(48, seed=Hq + d)
+    check_attention(*run_paged(attn, (Hq, Hkv, d, page, e4m3, new, lens, True, window), seed=d))
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_paged_attention_over_a_long_context_in_many_parts(attn, e4m3):
     """One KV head, one token: a single row of 160 key tiles is shared out over all SMs and merged;
