@@ -353,41 +353,60 @@ struct ReadParams {
   int max_pages, N;
 };
 
-// Four e4m3 codes times 2^(byte - 127), as two bf16x2 words, exact.  A code's exponent and
-// mantissa fields, shifted to where bf16 has its own, read as a bf16 of 2^-120 times the
-// code's value (subnormal codes too); the product with 2^(byte - 127 + 120) puts that
-// right.  lo and hi share that factor where it passes bf16's largest power.
-struct E4m3Scale {
-  __nv_bfloat162 lo, hi;
-  bool two;
-};
-__device__ __forceinline__ __nv_bfloat162 bf16x2_pow2(int e) {            // -133 <= e <= 127, as a pair
-  const uint32_t h = e >= -126 ? static_cast<uint32_t>(e + 127) << 7 : 1u << (e + 133);
-  const uint32_t w = h | (h << 16);
-  return *reinterpret_cast<const __nv_bfloat162*>(&w);
-}
-__device__ __forceinline__ E4m3Scale e4m3_scale(int byte) {
-  E4m3Scale s;
-  const int e = byte - 127 + 120;
-  s.two = e > 127;
-  s.lo = bf16x2_pow2(s.two ? 127 : e);
-  s.hi = bf16x2_pow2(s.two ? e - 127 : 0);
-  return s;
-}
-__device__ __forceinline__ uint32_t e4m3x2_widen(uint32_t x, const E4m3Scale& s) {
-  // x: two codes in the high bytes of its halves
-  const uint32_t w = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-  __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), s.lo);
-  if (s.two) v = __hmul2(v, s.hi);
-  // the two NaN codes (all ones) stay NaN
-  uint32_t r = *reinterpret_cast<uint32_t*>(&v);
-  if ((x & 0x7f000000u) == 0x7f000000u) r |= 0x7fc00000u;
-  if ((x & 0x00007f00u) == 0x00007f00u) r |= 0x00007fc0u;
+// e4m3 codes times 2^(byte - 127) as bf16, exact.  A code's exponent and mantissa fields,
+// shifted to where bf16 has its own, read as a bf16 of 2^-120 times the code's value
+// (subnormal codes too); the product with 2^(byte - 127 + 120) puts that right.  Two rare
+// things leave this path: the NaN codes, and scales whose factor passes bf16's largest
+// power (byte > 134), which takes two products.
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ void e4m3x4_widen(uint32_t codes, const E4m3Scale& s, uint32_t& w0, uint32_t& w1) {
-  w0 = e4m3x2_widen(__byte_perm(codes, 0, 0x1404), s);      // codes 0 and 1
-  w1 = e4m3x2_widen(__byte_perm(codes, 0, 0x3424), s);      // codes 2 and 3
+constexpr int kE4m3FastByte = 134;                         // factor 2^(byte - 7) up to 2^127
+__device__ __forceinline__ uint32_t e4m3_factor(int byte) { return static_cast<uint32_t>(byte + 120) * 0x00800080u; }
+__device__ __forceinline__ uint32_t e4m3_fields(uint32_t x) {      // two codes in the high bytes of the halves
+  return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+}
+// High bit of each byte that is a NaN code (all ones but the sign).
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t codes) { return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// Four codes with a factor, no NaN among them.
+__device__ __forceinline__ void e4m3x4_widen_fast(uint32_t codes, uint32_t f, uint32_t& w0, uint32_t& w1) {
+  w0 = bf16x2_mul(e4m3_fields(__byte_perm(codes, 0, 0x1404)), f);      // codes 0 and 1
+  w1 = bf16x2_mul(e4m3_fields(__byte_perm(codes, 0, 0x3424)), f);      // codes 2 and 3
+}
+// Any four codes under any scale byte.
+__device__ __noinline__ uint2 e4m3x4_widen_any(uint32_t codes, int byte) {
+  const int more = byte > kE4m3FastByte ? byte - kE4m3FastByte : 0;
+  uint32_t w[2];
+  e4m3x4_widen_fast(codes, e4m3_factor(byte - more), w[0], w[1]);
+  const uint32_t f2 = static_cast<uint32_t>(more + 127) * 0x00800080u, nan = e4m3_nans(codes);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (more) w[i] = bf16x2_mul(w[i], f2);
+    if (nan & (0x80u << (16 * i))) w[i] |= 0x00007fc0u;
+    if (nan & (0x8000u << (16 * i))) w[i] |= 0x7fc00000u;
+  }
+  return make_uint2(w[0], w[1]);
+}
+// N words of codes of one row.
+template <int N>
+__device__ __forceinline__ void e4m3_widen(const uint32_t (&codes)[N], int byte, uint32_t (&out)[2 * N]) {
+  uint32_t nan = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) nan |= (codes[i] & 0x7f7f7f7fu) + 0x01010101u;
+  if ((nan & 0x80808080u) == 0 && byte <= kE4m3FastByte) {
+    const uint32_t f = e4m3_factor(byte);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e4m3x4_widen_fast(codes[i], f, out[2 * i], out[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint2 w = e4m3x4_widen_any(codes[i], byte);
+      out[2 * i] = w.x;
+      out[2 * i + 1] = w.y;
+    }
+  }
 }
 
 // Grid: x over blocks of positions, y over (sequence, head).  A thread moves 16 output
@@ -430,11 +449,12 @@ __global__ void __launch_bounds__(256) attn_cache_read_kernel(const ReadParams p
     if constexpr (E4M3) {
       const uint2 kc = *reinterpret_cast<const uint2*>(p.c.k + src[i] + c * 8);
       const uint2 vc = *reinterpret_cast<const uint2*>(p.c.v + src[i] + c * 8);
-      const E4m3Scale ks = e4m3_scale(p.c.ks[at[i]]), vs = e4m3_scale(p.c.vs[at[i]]);
-      e4m3x4_widen(kc.x, ks, kx[i].x, kx[i].y);
-      e4m3x4_widen(kc.y, ks, kx[i].z, kx[i].w);
-      e4m3x4_widen(vc.x, vs, vx[i].x, vx[i].y);
-      e4m3x4_widen(vc.y, vs, vx[i].z, vx[i].w);
+      const uint32_t kw[2] = {kc.x, kc.y}, vw[2] = {vc.x, vc.y};
+      uint32_t ko[4], vo[4];
+      e4m3_widen<2>(kw, p.c.ks[at[i]], ko);
+      e4m3_widen<2>(vw, p.c.vs[at[i]], vo);
+      kx[i] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+      vx[i] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
     } else {
       kx[i] = *reinterpret_cast<const uint4*>(p.c.k + src[i] + c * 16);
       vx[i] = *reinterpret_cast<const uint4*>(p.c.v + src[i] + c * 16);

@@ -334,14 +334,15 @@ struct PagedCfg {
   static constexpr int kThreads = 320 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
   static constexpr int RST = KV8 ? (D == 128 ? 3 : 6) : 0;   // raw stages, K and V tiles alternating
-  static constexpr int kRawStage = kRawTile + 128;           // codes, then scale bytes
+  static constexpr int kRawStage = kRawTile;
   static constexpr int kS0 = 0, kS1 = 128, kO = 256;
   static constexpr int kTmemCols = 512;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = QST * kTile;
   static constexpr int kOffV = kOffK + KST * kTile;
   static constexpr int kOffRaw = kOffV + VST * kTile;
-  static constexpr int kOffSh = kOffRaw + ((RST * kRawStage + 127) / 128) * 128;
+  static constexpr int kOffScale = kOffRaw + RST * kRawStage;  // 128 scale bytes per raw stage
+  static constexpr int kOffSh = kOffScale + RST * 128;
   static constexpr int kLayout = kOffSh + 4608;
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 232448, "shared memory layout exceeds 227 KB");
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sV = smem + C::kOffV;
   uint8_t* sRaw = smem + C::kOffRaw;
+  uint8_t* sScale = smem + C::kOffScale;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
             if constexpr (KV8) {
               tma_load_4d(dst + r0 * D, kv ? &tmv : &tmk, full, 0, y, w.g, z);
               const long long pg = page < 0 ? 0 : page;         // scale bytes of some page of the pool
-              bulk_load(dst + C::kRawTile + r0,
+              bulk_load(sScale + st * 128 + r0,
                         (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y), rows, full);
             } else {
               tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? &tmv : &tmk, full, bc * 64, y, w.g, z);
@@ -641,11 +643,17 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
     // ------------------------------------------------------------ widening warps (e4m3 cache)
     // A lane takes 16 codes of a row, widens them with the row's scale and stores two
     // 16-byte chunks of the bf16 tile in the 128B-swizzled layout the TMA would write.
+    // Eight lanes (one shared-memory wavefront) take 4 chunks of each of 2 rows: their
+    // stores then fall on 8 different chunk positions.  At d = 128 the raw tile is
+    // swizzled too, and lanes 0-7 take the chunks {0, 5, 2, 7}, lanes 8-15 {1, 4, 3, 6} of
+    // their rows, for which the loads of both rows are disjoint as well.
     if constexpr (KV8) {
       const int wt = threadIdx.x - 320;             // 0 .. 32 * kWiden - 1
       constexpr int CPR = D / 16;                   // 16-code chunks per row
       constexpr int RPP = 32 * C::kWiden / CPR;     // rows per pass
-      const int c = wt % CPR;
+      const int e = wt & 3, half = (wt >> 3) & 1;   // chunk inside its set, which set (d = 128)
+      const int c = D == 128 ? (e ^ ((e & 1) << 2) ^ half) : e;
+      const int r_in = D == 128 ? ((wt >> 4) << 1) + ((wt >> 2) & 1) : wt >> 2;
       int kc = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
@@ -665,20 +673,21 @@ __global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
             uint8_t* out = (kv ? sV : sK) + st * C::kTile;
 #pragma unroll
             for (int r0 = 0; r0 < 128; r0 += RPP) {
-              const int r = r0 + wt / CPR;
-              uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
-              const E4m3Scale s = e4m3_scale(raw[C::kRawTile + r]);
-              uint4 a, b;
-              e4m3x4_widen(x.x, s, a.x, a.y);
-              e4m3x4_widen(x.y, s, a.z, a.w);
-              e4m3x4_widen(x.z, s, b.x, b.y);
-              e4m3x4_widen(x.w, s, b.z, b.w);
-              if (kv && (r < lo || r >= hi_row)) a = b = make_uint4(0u, 0u, 0u, 0u);   // keys that nobody sees
+              const int r = r0 + r_in;
+              const int rawc = D == 128 ? c ^ (r & 7) : c;
+              const uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + rawc * 16);
+              const uint32_t codes[4] = {x.x, x.y, x.z, x.w};
+              uint32_t y[8];
+              e4m3_widen<4>(codes, sScale[rs * 128 + r], y);
+              if (kv && (r < lo || r >= hi_row)) {  // keys that nobody sees
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = 0u;
+              }
               // chunks 2c and 2c + 1 of the row, 8 to a 64-column box
               const int box = c >> 2, cc = (2 * c) & 7;
               uint8_t* row = out + box * C::kBox + r * 128;
-              *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = a;
-              *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = b;
+              *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
             fence_proxy_async_smem();               // generic-proxy writes -> tensor-core reads
             __syncwarp();

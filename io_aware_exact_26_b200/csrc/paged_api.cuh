@@ -100,7 +100,8 @@ void launch_cache_read(const attn::ReadParams& p, int B, cudaStream_t s) {
 }
 
 // [num_pages][Hkv][page_size][d] as a 4-D map; one box is a page's (or 128 rows of it)
-// 64 bf16 columns, swizzled as the MMAs read them, or all e4m3 columns as they lie.
+// 64 bf16 columns, swizzled as the MMAs read them, or all e4m3 columns (swizzled at d = 128,
+// where a row is one 128-byte line, so that the widening warps read without conflicts).
 bool make_cache_map(CUtensorMap* m, const void* ptr, const attn_cache_t* c) {
   auto enc = encode_fn();
   if (!enc) return false;
@@ -114,7 +115,7 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, const attn_cache_t* c) {
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
              const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             elem == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             row >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
