@@ -376,7 +376,7 @@ __device__ __forceinline__ void e4m3x4_widen_fast(uint32_t codes, uint32_t f, ui
   w1 = bf16x2_mul(e4m3_fields(__byte_perm(codes, 0, 0x3424)), f);      // codes 2 and 3
 }
 // Any four codes under any scale byte.
-__device__ __noinline__ uint2 e4m3x4_widen_any(uint32_t codes, int byte) {
+__device__ __forceinline__ uint2 e4m3x4_widen_any(uint32_t codes, int byte) {
   const int more = byte > kE4m3FastByte ? byte - kE4m3FastByte : 0;
   uint32_t w[2];
   e4m3x4_widen_fast(codes, e4m3_factor(byte - more), w[0], w[1]);
@@ -389,18 +389,23 @@ __device__ __noinline__ uint2 e4m3x4_widen_any(uint32_t codes, int byte) {
   }
   return make_uint2(w[0], w[1]);
 }
-// N words of codes of one row.
+// Nonzero where one of the words has a NaN code.
 template <int N>
-__device__ __forceinline__ void e4m3_widen(const uint32_t (&codes)[N], int byte, uint32_t (&out)[2 * N]) {
+__device__ __forceinline__ uint32_t e4m3_any_nan(const uint32_t (&codes)[N]) {
   uint32_t nan = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) nan |= (codes[i] & 0x7f7f7f7fu) + 0x01010101u;
-  if ((nan & 0x80808080u) == 0 && byte <= kE4m3FastByte) {
+  return nan & 0x80808080u;
+}
+// N words of codes of one row; `rare`: a NaN code or a scale beyond kE4m3FastByte among them.
+template <int N>
+__device__ __forceinline__ void e4m3_widen(const uint32_t (&codes)[N], int byte, bool rare, uint32_t (&out)[2 * N]) {
+  if (!rare) {
     const uint32_t f = e4m3_factor(byte);
 #pragma unroll
     for (int i = 0; i < N; ++i) e4m3x4_widen_fast(codes[i], f, out[2 * i], out[2 * i + 1]);
   } else {
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       const uint2 w = e4m3x4_widen_any(codes[i], byte);
       out[2 * i] = w.x;
@@ -451,8 +456,9 @@ __global__ void __launch_bounds__(256) attn_cache_read_kernel(const ReadParams p
       const uint2 vc = *reinterpret_cast<const uint2*>(p.c.v + src[i] + c * 8);
       const uint32_t kw[2] = {kc.x, kc.y}, vw[2] = {vc.x, vc.y};
       uint32_t ko[4], vo[4];
-      e4m3_widen<2>(kw, p.c.ks[at[i]], ko);
-      e4m3_widen<2>(vw, p.c.vs[at[i]], vo);
+      const int kb = p.c.ks[at[i]], vb = p.c.vs[at[i]];
+      e4m3_widen<2>(kw, kb, kb > kE4m3FastByte || e4m3_any_nan<2>(kw), ko);
+      e4m3_widen<2>(vw, vb, vb > kE4m3FastByte || e4m3_any_nan<2>(vw), vo);
       kx[i] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
       vx[i] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
     } else {

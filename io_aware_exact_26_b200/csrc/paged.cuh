@@ -159,6 +159,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 __device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlan& pl, int cta) {
   const int nt = blockDim.x;
   long long mine = 0, incl = 0, total = 0, sum = 0;
+  if (threadIdx.x == 0) pl.b = p.B;           // nothing found yet; the scan's barriers order this first
   for (int b0 = 0; b0 < p.B; b0 += nt) {
     const int b = b0 + threadIdx.x;
     mine = 0;
@@ -178,7 +179,6 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlan& pl, 
     pl.parts = parts;
     pl.begin = begin;
     pl.end = end;
-    pl.b = p.B;
   }
   long long base = 0;
   for (int b0 = 0; b0 < p.B; b0 += nt) {      // again, to find the sequence that holds tile `begin`
@@ -272,6 +272,15 @@ struct PagedWalk {
   }
 };
 
+// mbar_wait without a look at the clock for the first tries: the waits on a tile's path
+// mostly end within them.
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity);
+}
+
 // Pieces passed from the producer warp to the consumer warps, in order.
 struct SegRing {
   uint64_t full[4];           // count 1
@@ -287,7 +296,7 @@ __device__ __forceinline__ void seg_ring_init(SegRing& r, uint32_t consumers) {
 // Producer (one thread): post the k-th piece; false if a wait failed.
 __device__ __forceinline__ bool seg_ring_post(SegRing& r, int k, const PagedSeg& w) {
   const int i = k & 3;
-  if (k >= 4 && !mbar_wait(&r.empty[i], ((k >> 2) - 1) & 1)) return false;
+  if (k >= 4 && !pipe_wait(&r.empty[i], ((k >> 2) - 1) & 1)) return false;
   r.seg[i] = w;
   mbar_arrive(&r.full[i]);
   return true;
@@ -297,7 +306,7 @@ __device__ __forceinline__ PagedSeg seg_ring_take(SegRing& r, int k, int lane, b
   const int i = k & 3;
   PagedSeg w;
   w.n = 0;
-  ok = __all_sync(0xffffffffu, mbar_wait(&r.full[i], (k >> 2) & 1));
+  ok = __all_sync(0xffffffffu, pipe_wait(&r.full[i], (k >> 2) & 1));
   if (!ok) return w;
   w = r.seg[i];
   __syncwarp();
@@ -318,58 +327,46 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* tmap, ui
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// ------------------------------------------------------------------ one query tile per CTA
-// Warps 0-7 softmax (two groups of 64 keys, thread = tile row = TMEM lane), warp 8
-// producer, warp 9 MMA issuer and, for an e4m3 cache, warps 10-17 that widen raw tiles to
-// bf16 ones.  TMEM: S in two buffers, so S of the next tile is computed while the softmax
-// works on this one, and O.
-template <int D, bool KV8>
-struct PagedCfg {
-  static constexpr int kTile = 128 * D * 2;
-  static constexpr int kBox = 128 * 128;
-  static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
-  static constexpr int QST = (KV8 && D == 128) ? 1 : 2;
-  static constexpr int KST = 2, VST = 2;
-  static constexpr int kWiden = KV8 ? 8 : 0;       // widening warps
-  static constexpr int kThreads = 320 + 32 * kWiden;
-  static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
-  static constexpr int RST = KV8 ? (D == 128 ? 3 : 6) : 0;   // raw stages, K and V tiles alternating
-  static constexpr int kRawStage = kRawTile;
-  static constexpr int kS0 = 0, kS1 = 128, kO = 256;
-  static constexpr int kTmemCols = 512;
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = QST * kTile;
-  static constexpr int kOffV = kOffK + KST * kTile;
-  static constexpr int kOffRaw = kOffV + VST * kTile;
-  static constexpr int kOffScale = kOffRaw + RST * kRawStage;  // 128 scale bytes per raw stage
-  static constexpr int kOffSh = kOffScale + RST * 128;
-  static constexpr int kLayout = kOffSh + 4608;
-  static constexpr int kSmem = kLayout + 1024;
-  static_assert(kSmem <= 232448, "shared memory layout exceeds 227 KB");
-};
-
-struct PagedShared {
-  float xmax[2][2][128];      // [parity of the quadrant's steps][group][row] partial row maxima
-  float xsum[2][128];
+// ------------------------------------------------------------------ pipeline shared by the kernels
+// Barriers between the producer warp, the widening warps (e4m3 cache) and the MMA warp.
+struct PagedPipe {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
   uint64_t raw_full[8], raw_empty[8];
-  uint64_t s_full[2], p_ready[2];
-  uint64_t pv_done[2];        // P V of step g complete, by g % 2: a waiter may be a step behind
-  uint64_t xbar[2][4];        // [parity][quadrant]: both groups' warps posted their maxima
-  uint64_t sbar[4];
-  uint64_t o_free;
   SegRing ring;
   uint64_t drain, teardown;
   PagedPlan plan;
   uint32_t tmem_base;
 };
-static_assert(sizeof(PagedShared) <= 4608, "PagedShared does not fit its slot");
+template <class C>
+__device__ __forceinline__ void paged_pipe_init(PagedPipe& sh, int ring_consumers, int warps) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&sh.q_full[i], 1);
+    mbar_init(&sh.q_empty[i], 1);
+  }
+  for (int i = 0; i < C::KST; ++i) {
+    mbar_init(&sh.k_full[i], C::KV8 ? C::kWiden : 1);
+    mbar_init(&sh.k_empty[i], 1);
+    mbar_init(&sh.v_full[i], C::KV8 ? C::kWiden : 1);
+    mbar_init(&sh.v_empty[i], 1);
+  }
+  for (int i = 0; i < C::RST; ++i) {
+    mbar_init(&sh.raw_full[i], 1);
+    mbar_init(&sh.raw_empty[i], C::kWiden);
+  }
+  seg_ring_init(sh.ring, ring_consumers);
+  mbar_init(&sh.drain, 1);
+  mbar_init(&sh.teardown, warps);
+}
 
-// Key tile j of a piece, page by page: lane i of the producer warp brings in the i-th
-// (page, 64-column box) of the tile.
+// Shared-memory regions of a kernel.
+struct PagedSmem {
+  uint8_t *q, *k, *v, *raw, *scale;
+};
+
+// Pages of a key tile that hold keys in [kmin, len): local indices.
 struct PageTile {
-  int first, count;           // pages of the tile that hold keys in [kmin, len): local indices
+  int first, count;
 };
 __device__ __forceinline__ PageTile page_tile(const PagedParams& p, const PagedSeg& w, int j) {
   const int lo = max(w.kmin, j * 128), hi = min(w.len, j * 128 + 128);
@@ -396,510 +393,220 @@ __device__ __forceinline__ int page_of(const PagedParams& p, const PagedSeg& w, 
   return page;
 }
 
-template <int D, bool KV8>
-__global__ void __launch_bounds__(PagedCfg<D, KV8>::kThreads, 1)
-    attn_paged_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv, const PagedParams p) {
-  using C = PagedCfg<D, KV8>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  PagedShared& sh = *reinterpret_cast<PagedShared*>(smem + C::kOffSh);
-  uint8_t* sQ = smem + C::kOffQ;
-  uint8_t* sK = smem + C::kOffK;
-  uint8_t* sV = smem + C::kOffV;
-  uint8_t* sRaw = smem + C::kOffRaw;
-  uint8_t* sScale = smem + C::kOffScale;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
-      mbar_init(&sh.k_full[i], KV8 ? C::kWiden : 1);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], KV8 ? C::kWiden : 1);
-      mbar_init(&sh.v_empty[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 8);
-      mbar_init(&sh.pv_done[i], 1);
-      for (int q = 0; q < 4; ++q) mbar_init(&sh.xbar[i][q], 2);
-    }
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], KV8 ? C::kWiden : 1);
-    }
-    for (int q = 0; q < 4; ++q) mbar_init(&sh.sbar[q], 2);
-    mbar_init(&sh.o_free, 8);
-    seg_ring_init(sh.ring, 9 + C::kWiden);
-    mbar_init(&sh.drain, 1);
-    mbar_init(&sh.teardown, 10 + C::kWiden);
-    fence_barrier_init();
+// Producer warp: walks through the CTA's share, posts its pieces and brings in Q, K and V
+// (K and V tiles alternating).  Lane 0 arms a stage's barrier, then lane i issues the copy
+// of the tile's i-th (page, 64-column box), so small pages cost no more issue time than
+// large ones; the table entries of the next tile are read while this one is on its way.
+template <class C>
+__device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tmq,
+                                              const CUtensorMap* tmk, const CUtensorMap* tmv, const PagedSmem& m,
+                                              int cta, int lane) {
+  if (lane == 0) {
+    tma_prefetch_desc(tmq); tma_prefetch_desc(tmk); tma_prefetch_desc(tmv);
+    p.cuts[cta].ntok = 0;
   }
-  if (warp == 0) { tmem_alloc(&sh.tmem_base, C::kTmemCols); tmem_relinquish(); }
-  grid_dependency_wait();
-  grid_dependency_launch();
-  paged_plan(p, sh.plan, cta);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem_base;
-
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer (whole warp)
-    if (lane == 0) {
-      tma_prefetch_desc(&tmq); tma_prefetch_desc(&tmk); tma_prefetch_desc(&tmv);
-      p.cuts[cta].ntok = 0;
-    }
-    __syncwarp();
-    PagedWalk walk;
-    walk.begin(p, sh.plan, lane);
-    const int psh = p.c.page_shift < 7 ? p.c.page_shift : 7;
-    const int rows = 1 << psh;                      // rows of a box
-    int kc = 0, nk = 0, uq = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const PagedSeg w = walk.next(p, sh.plan, cta);
-      if (lane == 0) ok = seg_ring_post(sh.ring, k, w);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok || w.n == 0) break;
-      if (lane == 0) {
-        const int qs = uq % C::QST;
-        if (uq >= C::QST) ok = mbar_wait(&sh.q_empty[qs], ((uq / C::QST) - 1) & 1);
-        if (ok) {
-          mbar_arrive_expect_tx(&sh.q_full[qs], p.G * p.R * D * 2);
-          for (int c = 0; c < C::NB; ++c)
-            tma_load_3d(sQ + qs * C::kTile + c * C::kBox, &tmq, &sh.q_full[qs], c * 64, w.g * p.G, w.tok0);
-        }
-      }
-      ++uq;
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      constexpr int NX = KV8 ? 1 : C::NB;           // column boxes per page
-      const int bx = lane / NX, bc = lane % NX;
-      int page = 0;
-      PageTile t = page_tile(p, w, w.j0);
-      if (ok && bx < t.count) page = page_of(p, w, w.j0, t.first + bx);
-      for (int j = 0; j < w.n && ok; ++j, ++kc) {
-        const int jt = w.j0 + j;
-        const PageTile tn = j + 1 < w.n ? page_tile(p, w, jt + 1) : PageTile{0, 0};
-        int page_n = 0;
-        if (bx < tn.count) page_n = page_of(p, w, jt + 1, tn.first + bx);     // in flight during this tile
-        const int y = p.c.page_shift > 7 ? (jt & ((1 << (p.c.page_shift - 7)) - 1)) * 128 : 0;
-        const int z = page < 0 ? p.c.num_pages : page;                        // outside the pool: zeros
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t *full, *empty;
-          uint8_t* dst;
-          int st, par;
-          bool wait;
-          if constexpr (KV8) {
-            const int rc = 2 * kc + kv;
-            st = rc % C::RST;
-            par = ((rc / C::RST) - 1) & 1;
-            wait = rc >= C::RST;
-            full = &sh.raw_full[st];
-            empty = &sh.raw_empty[st];
-            dst = sRaw + st * C::kRawStage;
-          } else {
-            st = kc & 1;
-            par = ((kc >> 1) - 1) & 1;
-            wait = kc >= 2;
-            full = kv ? &sh.v_full[st] : &sh.k_full[st];
-            empty = kv ? &sh.v_empty[st] : &sh.k_empty[st];
-            dst = (kv ? sV : sK) + st * C::kTile;
-          }
-          if (lane == 0) {
-            if (wait) ok = mbar_wait(empty, par);
-            if (ok) {
-              if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * (KV8 ? D + 1 : 2 * D));
-              else mbar_arrive(full);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          if (bx < t.count) {
-            const int r0 = (t.first + bx) << psh;    // row of the box in the tile
-            in_range(r0 + rows - 1, 128);
-            if constexpr (KV8) {
-              tma_load_4d(dst + r0 * D, kv ? &tmv : &tmk, full, 0, y, w.g, z);
-              const long long pg = page < 0 ? 0 : page;         // scale bytes of some page of the pool
-              bulk_load(sScale + st * 128 + r0,
-                        (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y), rows, full);
-            } else {
-              tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? &tmv : &tmk, full, bc * 64, y, w.g, z);
-            }
-          }
-          nk = KV8 ? 2 * kc + kv + 1 : 2 * kc + kv + 1;
-        }
-        page = page_n;
-        t = tn;
-      }
-    }
-    if (!ok && lane == 0) {                          // let copies in flight land
-      if constexpr (KV8) {
-        for (int r = max(0, nk - C::RST); r < nk; ++r) mbar_drain_wait(&sh.raw_full[r % C::RST], (r / C::RST) & 1);
-      } else {
-        for (int r = max(0, nk - 4); r < nk; ++r)
-          mbar_drain_wait((r & 1) ? &sh.v_full[(r >> 1) & 1] : &sh.k_full[(r >> 1) & 1], (r >> 2) & 1);
-      }
-      for (int r = max(0, uq - C::QST); r < uq; ++r) mbar_drain_wait(&sh.q_full[r % C::QST], (r / C::QST) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    // Per piece: S(0), S(1); then per step j: PV(j), S(j + 2) into the buffer PV(j) just
-    // read (MMAs of one thread run in issue order, so PV(j) reads P(j) first).
-    const bool leader = elect_one();
-    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
-    constexpr uint32_t hi = sdesc_hi_sw128(1024);
-    const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
-    const uint32_t k_lo0 = sdesc_lo(smem_u32(sK), 16);
-    const uint32_t v_lo0 = sdesc_lo(smem_u32(sV), C::kBox);
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-    };
-    int kc = 0, vc = 0, gs = 0, uq = 0;
-    bool ok = true;
-    auto issue_s = [&](int g, int qs) -> bool {     // S(g) = Q K(kc)^T into buffer g % 2
-      const int st = kc & 1;
-      if (!wait(&sh.k_full[st], (kc >> 1) & 1)) return false;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t q_lo = q_lo0 + qs * (C::kTile >> 4);
-        const uint32_t k_lo = k_lo0 + st * (C::kTile >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * C::kBox + (k & 3) * 32) >> 4;
-          umma_ss_lo(tmem + ((g & 1) ? C::kS1 : C::kS0), q_lo + off, k_lo + off, hi, idS, k > 0);
-        }
-        umma_commit(&sh.s_full[g & 1]);
-        umma_commit(&sh.k_empty[st]);
-      }
-      __syncwarp();
-      ++kc;
-      return true;
-    };
-    for (int k = 0; ok; ++k) {
-      const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
-      if (w.n == 0) break;
-      const int qs = uq % C::QST;
-      ok = wait(&sh.q_full[qs], (uq / C::QST) & 1);
-      for (int t = 0; t < 2 && t < w.n && ok; ++t) {
-        ok = issue_s(gs + t, qs);
-        if (ok && t == w.n - 1 && leader) umma_commit(&sh.q_empty[qs]);
-        __syncwarp();
-      }
-      for (int j = 0; j < w.n && ok; ++j, ++vc) {
-        const int g = gs + j, vst = vc & 1;
-        ok = wait(&sh.v_full[vst], (vc >> 1) & 1);
-        if constexpr (!KV8) {
-          // Rows of V at keys that nobody sees (behind the sequence, before the window, in
-          // pages that were not loaded) are zeroed: their P is 0, and 0 times whatever lies
-          // there has to be 0.
-          const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
-          if (ok && (lo > 0 || hi_row < 128)) {
-            uint8_t* v = sV + vst * C::kTile;
-            for (int x = lane; x < 128 * 8; x += 32) {
-              const int r = x >> 3;
-              if (r >= lo && r < hi_row) continue;
-              for (int c = 0; c < C::NB; ++c)
-                *reinterpret_cast<uint4*>(v + c * C::kBox + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (ok) ok = wait(&sh.p_ready[g & 1], (g >> 1) & 1);
-        if (ok && j == 0 && uq >= 1) ok = wait(&sh.o_free, (uq - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t v_lo = v_lo0 + vst * (C::kTile >> 4);
-          const uint32_t sbase = tmem + ((g & 1) ? C::kS1 : C::kS0);
-#pragma unroll
-          for (int k2 = 0; k2 < 8; ++k2)
-            umma_ts_lo(tmem + C::kO, sbase + (k2 >> 2) * 64 + (k2 & 3) * 8, v_lo + ((k2 * 2048) >> 4), hi, idO,
-                       !(j == 0 && k2 == 0));
-          umma_commit(&sh.pv_done[g & 1]);
-          umma_commit(&sh.v_empty[vst]);
-        }
-        __syncwarp();
-        if (j + 2 < w.n) {
-          ok = issue_s(g + 2, qs);
-          if (ok && j + 2 == w.n - 1 && leader) umma_commit(&sh.q_empty[qs]);
-          __syncwarp();
-        }
-      }
-      gs += w.n;
-      ++uq;
-    }
-    if (leader) {
-      umma_commit(&sh.drain);
-      mbar_wait(&sh.drain, 0);
-    }
-    __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ widening warps (e4m3 cache)
-    // A lane takes 16 codes of a row, widens them with the row's scale and stores two
-    // 16-byte chunks of the bf16 tile in the 128B-swizzled layout the TMA would write.
-    // Eight lanes (one shared-memory wavefront) take 4 chunks of each of 2 rows: their
-    // stores then fall on 8 different chunk positions.  At d = 128 the raw tile is
-    // swizzled too, and lanes 0-7 take the chunks {0, 5, 2, 7}, lanes 8-15 {1, 4, 3, 6} of
-    // their rows, for which the loads of both rows are disjoint as well.
-    if constexpr (KV8) {
-      const int wt = threadIdx.x - 320;             // 0 .. 32 * kWiden - 1
-      constexpr int CPR = D / 16;                   // 16-code chunks per row
-      constexpr int RPP = 32 * C::kWiden / CPR;     // rows per pass
-      const int e = wt & 3, half = (wt >> 3) & 1;   // chunk inside its set, which set (d = 128)
-      const int c = D == 128 ? (e ^ ((e & 1) << 2) ^ half) : e;
-      const int r_in = D == 128 ? ((wt >> 4) << 1) + ((wt >> 2) & 1) : wt >> 2;
-      int kc = 0;
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
-        if (w.n == 0) break;
-        for (int j = 0; j < w.n && ok; ++j, ++kc) {
-          const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
-          const int st = kc & 1;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const int rc = 2 * kc + kv, rs = rc % C::RST;
-            ok = __all_sync(0xffffffffu, mbar_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
-            if (ok && kc >= 2)
-              ok = __all_sync(0xffffffffu, mbar_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], ((kc >> 1) - 1) & 1));
-            if (!ok) break;
-            const uint8_t* raw = sRaw + rs * C::kRawStage;
-            uint8_t* out = (kv ? sV : sK) + st * C::kTile;
-#pragma unroll
-            for (int r0 = 0; r0 < 128; r0 += RPP) {
-              const int r = r0 + r_in;
-              const int rawc = D == 128 ? c ^ (r & 7) : c;
-              const uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + rawc * 16);
-              const uint32_t codes[4] = {x.x, x.y, x.z, x.w};
-              uint32_t y[8];
-              e4m3_widen<4>(codes, sScale[rs * 128 + r], y);
-              if (kv && (r < lo || r >= hi_row)) {  // keys that nobody sees
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = 0u;
-              }
-              // chunks 2c and 2c + 1 of the row, 8 to a 64-column box
-              const int box = c >> 2, cc = (2 * c) & 7;
-              uint8_t* row = out + box * C::kBox + r * 128;
-              *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-            fence_proxy_async_smem();               // generic-proxy writes -> tensor-core reads
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(kv ? &sh.v_full[st] : &sh.k_full[st]);
-              mbar_arrive(&sh.raw_empty[rs]);
-            }
-          }
-        }
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ softmax warps 0-7
-    const int grp = warp >> 2;                                  // keys [64 grp, 64 grp + 64)
-    const int quad = warp & 3;
-    const int row = quad * 32 + lane;                           // tile row = TMEM lane
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    constexpr int OH = D / 2;
-    const uint32_t o_base = lane_base + C::kO + grp * OH;
-    const float c = p.cs;
-    const uint64_t c2 = f2pack(c, c);
-    const int i = row / p.G, h = row - i * p.G;                 // token of the tile, head of the group
-    int gs = 0, uq = 0;
-    int xs = 0;                 // steps in which this quadrant had rows: its maxima barriers' count
-    bool ok = true;
-    auto mask16 = [&](uint32_t (&r)[16], int col0, int lo, int lim) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (col0 + k < lo || col0 + k > lim) r[k] = 0xff800000u;
-    };
-    for (int k = 0; ok; ++k) {
-      const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
-      if (w.n == 0) break;
-      const bool valid = i < w.ntok && row < p.G * p.R;
-      const bool active = __any_sync(0xffffffffu, valid);       // a warp without rows only keeps step
-      const int pos = w.pos0 + i;
-      const int lastk = p.causal ? min(w.len - 1, pos) : w.len - 1;
-      const int firstk = p.wl >= 0 ? pos - p.wl : 0;
-      float m_used = -INFINITY;
-      uint64_t lsum = f2pack(0.f, 0.f);
-      for (int j = 0; j < w.n && ok; ++j) {
-        const int g2 = gs + j, xp = xs & 1;
-        const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 64;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g2 & 1], (g2 >> 1) & 1));
-        if (!ok) break;
-        if (!active) {
-          if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
-          __syncwarp();
-          continue;
-        }
-        tc_fence_after();
-        const int kbase = (w.j0 + j) * 128 + grp * 64;
-        const int lo = firstk - kbase, lim = lastk - kbase;        // visible columns [lo, lim]
-        const bool msk = __any_sync(0xffffffffu, valid && (lo > 0 || lim < 63));
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        {
-          uint32_t r0[16], r1[16], r2[16], r3[16];
-          tmem_ld16(s_base, r0);
-          tmem_ld16(s_base + 16, r1);
-          tmem_ld16(s_base + 32, r2);
-          tmem_ld16(s_base + 48, r3);
-          tmem_wait_ld();
-          reg_fence(r0);
-          reg_fence(r1);
-          reg_fence(r2);
-          reg_fence(r3);
-          if (msk) { mask16(r0, 0, lo, lim); mask16(r1, 16, lo, lim); mask16(r2, 32, lo, lim); mask16(r3, 48, lo, lim); }
-#pragma unroll
-          for (int kk = 0; kk < 16; kk += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              mx4[e] = max3f(mx4[e], __uint_as_float(r0[kk + e]), __uint_as_float(r0[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r1[kk + e]), __uint_as_float(r1[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r2[kk + e]), __uint_as_float(r2[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r3[kk + e]), __uint_as_float(r3[kk + e + 4]));
-            }
-          }
-        }
-        sh.xmax[xp][grp][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.xbar[xp][quad]);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[xp][quad], (xs >> 1) & 1));
-        if (!ok) break;
-        ++xs;
-        const float mx = fmaxf(sh.xmax[xp][0][row], sh.xmax[xp][1][row]);
-        const float m_tile = mx == -INFINITY ? -INFINITY : mx * c;
-        float alpha = 1.f;
-        // a row that has seen no key keeps m_used = -inf (and p = 0) until it sees one
-        const bool need = valid && m_tile > m_used + kRescaleTau;
-        if (need) {
-          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx(m_used - m_tile);
-          float l0, l1;
-          f2unpack(lsum, l0, l1);
-          lsum = f2pack(l0 * alpha, l1 * alpha);
-          m_used = m_tile;
-        }
-        // S(j) was issued before PV(j - 1) (and after PV(j - 2), which its commit covers):
-        // wait for PV(j - 1) before rescaling O
-        if (__any_sync(0xffffffffu, need && j > 0)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g2 - 1) & 1], ((g2 - 1) >> 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int q4 = 0; q4 < OH / 16; ++q4) {
-            uint32_t o[16];
-            tmem_ld16(o_base + q4 * 16, o);
-            tmem_wait_ld();
-            reg_fence(o);
-#pragma unroll
-            for (int kk = 0; kk < 16; ++kk)
-              o[kk] = alpha == 0.f ? 0u : __float_as_uint(__uint_as_float(o[kk]) * alpha);
-            tmem_st16(o_base + q4 * 16, o);
-          }
-        }
-        const float mb = m_used == -INFINITY ? 0.f : m_used;
-        const uint64_t nm2 = f2pack(-mb, -mb);
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t r[16];
-          tmem_ld16(s_base + cc * 16, r);
-          tmem_wait_ld();
-          reg_fence(r);
-          if (msk) mask16(r, cc * 16, lo, lim);
-          uint32_t pk[8];
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t xx =
-                ffma2(f2pack(__uint_as_float(r[2 * kk]), __uint_as_float(r[2 * kk + 1])), c2, nm2);
-            float x0, x1;
-            f2unpack(xx, x0, x1);
-            const float a0 = ex2_approx(x0), a1 = ex2_approx(x1);
-            lsum = fadd2(lsum, f2pack(a0, a1));
-            pk[kk] = pack_bf16x2(a0, a1);
-          }
-          tmem_st8(s_base + cc * 8, pk);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
-      }
-      if (!ok) break;
-      // epilogue: the two groups' sums, the last PV, O / l and the LSE of this piece
-      const int glast = gs + w.n - 1;
-      float l = 0.f;
-      if (active) {
-        float l0, l1;
-        f2unpack(lsum, l0, l1);
-        sh.xsum[grp][row] = l0 + l1;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.sbar[quad]);
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar[quad], uq & 1));
-      if (!ok) break;
-      if (active) l = sh.xsum[0][row] + sh.xsum[1][row];
-      // PV(glast): S(glast) covered PV(glast - 2), the one before it on this barrier, so the
-      // parity is unambiguous (a parity wait tells apart two successive phases only)
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
-      if (!ok) break;
-      if (active) {
-        tc_fence_after();
-        const bool none = l == 0.f;                               // no key seen
-        const float inv_l = none ? 0.f : 1.f / l;
-        const float lse_s = none ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
-        const size_t orow = static_cast<size_t>(w.tok0 + i) * p.Hq + w.g * p.G + h;
-        const bool store = valid && in_range(w.tok0 + i, p.T) && in_range(row, w.slot < 0 ? 128 : p.slot_rows);
-#pragma unroll 1
-        for (int q4 = 0; q4 < OH / 16; ++q4) {
-          uint32_t o[16];
-          tmem_ld16(o_base + q4 * 16, o);
-          tmem_wait_ld();
-          reg_fence(o);
-          if (!store) continue;
-          float f[16];
-#pragma unroll
-          for (int kk = 0; kk < 16; ++kk) f[kk] = none ? 0.f : __uint_as_float(o[kk]) * inv_l;
-          if (w.slot < 0) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) pk[kk] = pack_bf16x2(f[2 * kk], f[2 * kk + 1]);
-            uint4* dst = reinterpret_cast<uint4*>(p.o + orow * D + grp * OH + q4 * 16);
-            dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(
-                p.opart + (static_cast<size_t>(w.slot) * p.slot_rows + row) * D + grp * OH + q4 * 16);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              dst[kk] = make_float4(f[4 * kk], f[4 * kk + 1], f[4 * kk + 2], f[4 * kk + 3]);
-          }
-        }
-        if (store && grp == 0) {
-          if (w.slot < 0) p.lse[orow] = lse_s;
-          else p.lpart[static_cast<size_t>(w.slot) * p.slot_rows + row] = lse_s;
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_free);
-      gs += w.n;
-      ++uq;
-    }
-  }
-
-  tc_fence_before();
   __syncwarp();
-  if (lane == 0) mbar_arrive(&sh.teardown);
-  if (warp == 0) {
-    mbar_wait(&sh.teardown, 0);
-    tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+  PagedWalk walk;
+  walk.begin(p, sh.plan, lane);
+  const int psh = p.c.page_shift < 7 ? p.c.page_shift : 7;
+  const int rows = 1 << psh;                        // rows of a box
+  constexpr int NX = C::KV8 ? 1 : C::NB;            // column boxes per page
+  const int bx = lane / NX, bc = lane % NX;
+  int kc = 0, nk = 0, uq = 0;                       // key tiles, K/V stages armed, pieces
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const PagedSeg w = walk.next(p, sh.plan, cta);
+    int page = 0;
+    PageTile t{0, 0};
+    if (w.n > 0) {
+      t = page_tile(p, w, w.j0);
+      if (bx < t.count) page = page_of(p, w, w.j0, t.first + bx);
+    }
+    if (lane == 0) {
+      ok = seg_ring_post(sh.ring, k, w);
+      if (ok && w.n > 0) {
+        const int qs = uq % C::QST;
+        if (uq >= C::QST) ok = pipe_wait(&sh.q_empty[qs], ((uq / C::QST) - 1) & 1);
+        if (ok) {
+          mbar_arrive_expect_tx(&sh.q_full[qs], p.G * p.R * C::D * 2);
+          for (int c = 0; c < C::NB; ++c)
+            tma_load_3d(m.q + qs * C::kQTile + c * C::kQBox, tmq, &sh.q_full[qs], c * 64, w.g * p.G, w.tok0);
+          ++uq;
+        }
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (!ok || w.n == 0) break;
+    for (int j = 0; j < w.n && ok; ++j, ++kc) {
+      const int jt = w.j0 + j;
+      PageTile tn{0, 0};
+      int page_n = 0;
+      if (j + 1 < w.n) {
+        tn = page_tile(p, w, jt + 1);
+        if (bx < tn.count) page_n = page_of(p, w, jt + 1, tn.first + bx);     // in flight during this tile
+      }
+      const int y = p.c.page_shift > 7 ? (jt & ((1 << (p.c.page_shift - 7)) - 1)) * 128 : 0;
+      const int z = page < 0 ? p.c.num_pages : page;                          // outside the pool: zeros
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint64_t *full, *empty;
+        uint8_t* dst;
+        int st, round;                              // stage, and which use of it this is
+        if constexpr (C::KV8) {
+          const int rc = 2 * kc + kv;
+          st = rc % C::RST;
+          round = rc / C::RST;
+          full = &sh.raw_full[st];
+          empty = &sh.raw_empty[st];
+          dst = m.raw + st * C::kRawTile;
+        } else {
+          st = kc % C::KST;
+          round = kc / C::KST;
+          full = kv ? &sh.v_full[st] : &sh.k_full[st];
+          empty = kv ? &sh.v_empty[st] : &sh.k_empty[st];
+          dst = (kv ? m.v : m.k) + st * C::kTile;
+        }
+        if (lane == 0) {
+          if (round > 0) ok = pipe_wait(empty, (round - 1) & 1);
+          if (ok) {
+            if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * (C::KV8 ? C::D + 1 : 2 * C::D));
+            else mbar_arrive(full);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        if (bx < t.count) {
+          const int r0 = (t.first + bx) << psh;     // row of the box in the tile
+          in_range(r0 + rows - 1, 128);
+          if constexpr (C::KV8) {
+            tma_load_4d(dst + r0 * C::D, kv ? tmv : tmk, full, 0, y, w.g, z);
+            const long long pg = page < 0 ? 0 : page;          // scale bytes of some page of the pool
+            bulk_load(m.scale + st * 128 + r0, (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y),
+                      rows, full);
+          } else {
+            tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? tmv : tmk, full, bc * 64, y, w.g, z);
+          }
+        }
+        nk = 2 * kc + kv + 1;
+      }
+      page = page_n;
+      t = tn;
+    }
   }
+  if (!ok && lane == 0) {                           // let copies in flight land
+    for (int r = max(0, nk - (C::KV8 ? C::RST : 2 * C::KST)); r < nk; ++r) {
+      if constexpr (C::KV8) {
+        mbar_drain_wait(&sh.raw_full[r % C::RST], (r / C::RST) & 1);
+      } else {
+        const int kt = r >> 1;
+        mbar_drain_wait((r & 1) ? &sh.v_full[kt % C::KST] : &sh.k_full[kt % C::KST], (kt / C::KST) & 1);
+      }
+    }
+    for (int r = max(0, uq - C::QST); r < uq; ++r) mbar_drain_wait(&sh.q_full[r % C::QST], (r / C::QST) & 1);
+  }
+  __syncwarp();
+}
+
+// Widening warps (e4m3 cache), wt = 0 .. 32 kWiden - 1.  A lane takes 16 codes of a row,
+// widens them with the row's scale and stores two 16-byte chunks of the bf16 tile in the
+// 128B-swizzled layout the TMA would write.  Eight lanes (one shared-memory wavefront)
+// take 4 chunks of each of 2 rows: their stores then fall on 8 different chunk positions.
+// At d = 128 the raw tile is swizzled too, and lanes 0-7 take the chunks {0, 5, 2, 7},
+// lanes 8-15 {1, 4, 3, 6} of their rows, for which the loads of both rows are disjoint as
+// well (without this, 30% more time per tile).
+template <class C>
+__device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, int wt, int lane) {
+  constexpr int D = C::D;
+  constexpr int CPR = D / 16;                       // 16-code chunks per row
+  constexpr int RPP = 32 * C::kWiden / CPR;         // rows per pass
+  const int e = wt & 3, half = (wt >> 3) & 1;       // chunk inside its set, which set (d = 128)
+  const int c = D == 128 ? (e ^ ((e & 1) << 2) ^ half) : e;
+  const int r_in = D == 128 ? ((wt >> 4) << 1) + ((wt >> 2) & 1) : wt >> 2;
+  int kc = 0;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
+    if (w.n == 0) break;
+    for (int j = 0; j < w.n && ok; ++j, ++kc) {
+      const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
+      const int st = kc % C::KST;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int rc = 2 * kc + kv, rs = rc % C::RST;
+        ok = __all_sync(0xffffffffu, pipe_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
+        if (ok && kc >= C::KST)
+          ok = __all_sync(0xffffffffu, pipe_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], ((kc / C::KST) - 1) & 1));
+        if (!ok) break;
+        const uint8_t* raw = m.raw + rs * C::kRawTile;
+        uint8_t* out = (kv ? m.v : m.k) + st * C::kTile;
+        constexpr int NP = 128 / RPP;               // passes
+        uint32_t codes[NP][4];
+        int byte[NP];
+        bool rare = false;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {              // all loads first
+          const int r = i * RPP + r_in, rawc = D == 128 ? c ^ (r & 7) : c;
+          const uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + rawc * 16);
+          codes[i][0] = x.x; codes[i][1] = x.y; codes[i][2] = x.z; codes[i][3] = x.w;
+          byte[i] = m.scale[rs * 128 + r];
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int r = i * RPP + r_in;
+          if (kv && (r < lo || r >= hi_row)) {      // keys that nobody sees
+            codes[i][0] = codes[i][1] = codes[i][2] = codes[i][3] = 0u;
+            byte[i] = 0;
+          }
+          rare |= byte[i] > kE4m3FastByte || e4m3_any_nan<4>(codes[i]) != 0;
+        }
+        rare = __any_sync(0xffffffffu, rare);       // one branch for the warp and the tile
+        auto put = [&](int i, const uint32_t (&y)[8]) {
+          // chunks 2c and 2c + 1 of the row, 8 to a 64-column box
+          const int r = i * RPP + r_in, box = c >> 2, cc = (2 * c) & 7;
+          uint8_t* row = out + box * C::kBox + r * 128;
+          *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        };
+        if (!rare) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            uint32_t y[8];
+            e4m3_widen<4>(codes[i], byte[i], false, y);
+            put(i, y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            uint32_t y[8];
+            e4m3_widen<4>(codes[i], byte[i], true, y);
+            put(i, y);
+          }
+        }
+        fence_proxy_async_smem();                   // generic-proxy writes -> tensor-core reads
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv ? &sh.v_full[st] : &sh.k_full[st]);
+          mbar_arrive(&sh.raw_empty[rs]);
+        }
+      }
+    }
+  }
+}
+
+// Rows of a bf16 V tile at keys that nobody sees (behind the sequence, before the window,
+// in pages that were not loaded) are zeroed by the MMA warp: their P is 0, and 0 times
+// whatever lies there has to be 0.
+template <class C>
+__device__ __forceinline__ void paged_zero_v(const PagedSeg& w, int j, uint8_t* v, int lane) {
+  const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
+  if (lo <= 0 && hi_row >= 128) return;
+  for (int x = lane; x < 128 * 8; x += 32) {
+    const int r = x >> 3;
+    if (r >= lo && r < hi_row) continue;
+    for (int c = 0; c < C::NB; ++c) *reinterpret_cast<uint4*>(v + c * C::kBox + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // Merge of cut items: block x looks after the item whose first part CTA x holds, the

@@ -2,7 +2,8 @@
 // operators.  Included by api.cu, whose device query, alignment test and encoder it uses.
 #pragma once
 #include "attn_paged.h"
-#include "paged.cuh"
+#include "paged_few.cuh"
+#include "paged_rows.cuh"
 
 namespace {
 
@@ -151,15 +152,22 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int sme
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Query rows per item, by the batch's mean: 16 or 32 of the kernel for few rows where a
+// sequence's rows fit, else 128.  Any form is right for any lengths.
+int paged_form(int T, int B, int G) {
+  const long long rows = static_cast<long long>(G) * ((T + B - 1) / B);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+}
+
 // Workspace of the cut items: descriptors, LSE of the parts, then their O (fp32).
 struct PagedWs {
   int slot_rows;
   size_t l_off, o_off, total;
 };
-PagedWs paged_ws(int T, int G, int d, int sms) {
+PagedWs paged_ws(int T, int G, int form, int d, int sms) {
   PagedWs w;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const long long R = 128 / G;
+  const long long R = form / G;
   w.slot_rows = static_cast<int>((T < R ? T : R) * G);
   w.l_off = up(sizeof(attn::PagedCut) * sms);
   w.o_off = up(w.l_off + static_cast<size_t>(2) * sms * w.slot_rows * 4);
@@ -174,25 +182,37 @@ int check_paged_heads(int T, int B, int Hq, int Hkv, int d) {
   return ATTN_OK;
 }
 
-template <int D, bool KV8>
-int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const attn::PagedParams& p,
-                 int merge_rows, cudaStream_t stream) {
-  using C = attn::PagedCfg<D, KV8>;
+// C: the kernel's configuration.
+template <class C, typename Kernel>
+int launch_paged(Kernel kernel, const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache,
+                 const attn::PagedParams& p, cudaStream_t stream) {
   static std::once_flag attr_once[64];
   static bool attr_ok[64];
   int dev = 0;
   cudaGetDevice(&dev);
   std::call_once(attr_once[dev], [&] {
-    attr_ok[dev] = cudaFuncSetAttribute(attn::attn_paged_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        C::kSmem) == cudaSuccess;
+    attr_ok[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess;
   });
   if (!attr_ok[dev]) return ATTN_ERR_LAUNCH;
-  if (launch_pdl(attn::attn_paged_kernel<D, KV8>, dim3(p.ctas), C::kThreads, C::kSmem, stream, tq, tk, tv, p) !=
-      cudaSuccess)
+  CUtensorMap tq, tk, tv;
+  if (!make_q_map(&tq, q, q_strides, p.T, p.Hq, cache->d, p.G, p.R) || !make_cache_map(&tk, cache->k, cache) ||
+      !make_cache_map(&tv, cache->v, cache))
     return ATTN_ERR_LAUNCH;
-  const dim3 grid(p.ctas, (merge_rows + 15) / 16);
-  if (launch_pdl(attn::attn_paged_merge_kernel<D>, grid, 128, 0, stream, p) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  if (launch_pdl(kernel, dim3(p.ctas), C::kThreads, C::kSmem, stream, tq, tk, tv, p) != cudaSuccess)
+    return ATTN_ERR_LAUNCH;
+  const dim3 grid(p.ctas, (p.slot_rows + 15) / 16);
+  if (launch_pdl(attn::attn_paged_merge_kernel<C::D>, grid, 128, 0, stream, p) != cudaSuccess) return ATTN_ERR_LAUNCH;
   return ATTN_OK;
+}
+
+template <int D, bool KV8>
+int launch_paged_form(int form, const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache,
+                      const attn::PagedParams& p, cudaStream_t s) {
+  if (form == 16)
+    return launch_paged<attn::FewCfg<D, KV8, 16>>(attn::attn_paged_few_kernel<D, KV8, 16>, q, q_strides, cache, p, s);
+  if (form == 32)
+    return launch_paged<attn::FewCfg<D, KV8, 32>>(attn::attn_paged_few_kernel<D, KV8, 32>, q, q_strides, cache, p, s);
+  return launch_paged<attn::RowsCfg<D, KV8>>(attn::attn_paged_rows_kernel<D, KV8>, q, q_strides, cache, p, s);
 }
 
 }  // namespace
@@ -338,7 +358,7 @@ size_t attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d) {
   if (check_paged_heads(T, B, Hq, Hkv, d) != ATTN_OK || T == 0) return 0;
   DeviceInfo* di = nullptr;
   if (device_info(&di) != 0) return 0;
-  return paged_ws(T, Hq / Hkv, d, di->sms).total;
+  return paged_ws(T, Hq / Hkv, paged_form(T, B, Hq / Hkv), d, di->sms).total;
 }
 
 int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache, const attn_batch_t* batch,
@@ -356,12 +376,9 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   DeviceInfo* di = nullptr;
   if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
   const int d = cache->d, G = Hq / cache->Hkv;
-  const PagedWs W = paged_ws(batch->T, G, d, di->sms);
+  const int form = paged_form(batch->T, batch->B, G);
+  const PagedWs W = paged_ws(batch->T, G, form, d, di->sms);
   if (workspace && workspace_bytes < W.total) return ATTN_ERR_WORKSPACE;
-  CUtensorMap tq, tk, tv;
-  if (!make_q_map(&tq, q, q_strides, batch->T, Hq, d, G, 128 / G) || !make_cache_map(&tk, cache->k, cache) ||
-      !make_cache_map(&tv, cache->v, cache))
-    return ATTN_ERR_LAUNCH;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = workspace;
   if (!ws && cudaMallocAsync(&ws, W.total, s) != cudaSuccess) {
@@ -381,7 +398,7 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   p.Hq = Hq;
   p.Hkv = cache->Hkv;
   p.G = G;
-  p.R = 128 / G;
+  p.R = form / G;
   p.RI = p.R;
   p.causal = causal;
   p.wl = window_left < 0 ? -1 : window_left;
@@ -394,9 +411,11 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   p.opart = reinterpret_cast<float*>(static_cast<char*>(ws) + W.o_off);
   int st2;
   if (cache->dtype == ATTN_E4M3)
-    st2 = d == 64 ? launch_paged<64, true>(tq, tk, tv, p, W.slot_rows, s) : launch_paged<128, true>(tq, tk, tv, p, W.slot_rows, s);
+    st2 = d == 64 ? launch_paged_form<64, true>(form, q, q_strides, cache, p, s)
+                  : launch_paged_form<128, true>(form, q, q_strides, cache, p, s);
   else
-    st2 = d == 64 ? launch_paged<64, false>(tq, tk, tv, p, W.slot_rows, s) : launch_paged<128, false>(tq, tk, tv, p, W.slot_rows, s);
+    st2 = d == 64 ? launch_paged_form<64, false>(form, q, q_strides, cache, p, s)
+                  : launch_paged_form<128, false>(form, q, q_strides, cache, p, s);
   if (!workspace && cudaFreeAsync(ws, s) != cudaSuccess) {
     (void)cudaGetLastError();
     return st2 != ATTN_OK ? st2 : ATTN_ERR_ALLOC;
