@@ -363,17 +363,22 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t prmt_b32(uint32_t a, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(a), "r"(sel));
+  return r;
+}
 constexpr int kE4m3FastByte = 134;                         // factor 2^(byte - 7) up to 2^127
 __device__ __forceinline__ uint32_t e4m3_factor(int byte) { return static_cast<uint32_t>(byte + 120) * 0x00800080u; }
-__device__ __forceinline__ uint32_t e4m3_fields(uint32_t x) {      // two codes in the high bytes of the halves
-  return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-}
+// Two codes, each sign-extended to 16 bits, to those fields (sign in bit 15, the rest from
+// bit 4 up).  prmt's selectors 8 + i replicate the sign of byte i.
+__device__ __forceinline__ uint32_t e4m3_fields(uint32_t x) { return (x << 4) & 0x87f087f0u; }
 // High bit of each byte that is a NaN code (all ones but the sign).
 __device__ __forceinline__ uint32_t e4m3_nans(uint32_t codes) { return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 // Four codes with a factor, no NaN among them.
 __device__ __forceinline__ void e4m3x4_widen_fast(uint32_t codes, uint32_t f, uint32_t& w0, uint32_t& w1) {
-  w0 = bf16x2_mul(e4m3_fields(__byte_perm(codes, 0, 0x1404)), f);      // codes 0 and 1
-  w1 = bf16x2_mul(e4m3_fields(__byte_perm(codes, 0, 0x3424)), f);      // codes 2 and 3
+  w0 = bf16x2_mul(e4m3_fields(prmt_b32(codes, 0x9180)), f);      // codes 0 and 1
+  w1 = bf16x2_mul(e4m3_fields(prmt_b32(codes, 0xb3a2)), f);      // codes 2 and 3
 }
 // Any four codes under any scale byte.
 __device__ __forceinline__ uint2 e4m3x4_widen_any(uint32_t codes, int byte) {
@@ -405,7 +410,7 @@ __device__ __forceinline__ void e4m3_widen(const uint32_t (&codes)[N], int byte,
 #pragma unroll
     for (int i = 0; i < N; ++i) e4m3x4_widen_fast(codes[i], f, out[2 * i], out[2 * i + 1]);
   } else {
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint2 w = e4m3x4_widen_any(codes[i], byte);
       out[2 * i] = w.x;

@@ -530,7 +530,7 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
     for (int j = 0; j < w.n && ok; ++j, ++kc) {
       const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
       const int st = kc % C::KST;
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int rc = 2 * kc + kv, rs = rc % C::RST;
         ok = __all_sync(0xffffffffu, pipe_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
@@ -540,34 +540,33 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
         const uint8_t* raw = m.raw + rs * C::kRawTile;
         uint8_t* out = (kv ? m.v : m.k) + st * C::kTile;
         constexpr int NP = 128 / RPP;               // passes
-        uint32_t codes[NP][4];
-        int byte[NP];
-        bool rare = false;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {              // all loads first
-          const int r = i * RPP + r_in, rawc = D == 128 ? c ^ (r & 7) : c;
+        auto at = [&](int i) { return i * RPP + r_in; };
+        auto load = [&](int i, uint32_t (&codes)[4], int& byte) {
+          const int r = at(i), rawc = D == 128 ? c ^ (r & 7) : c;
           const uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + rawc * 16);
-          codes[i][0] = x.x; codes[i][1] = x.y; codes[i][2] = x.z; codes[i][3] = x.w;
-          byte[i] = m.scale[rs * 128 + r];
-        }
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int r = i * RPP + r_in;
+          codes[0] = x.x; codes[1] = x.y; codes[2] = x.z; codes[3] = x.w;
+          byte = m.scale[rs * 128 + r];
           if (kv && (r < lo || r >= hi_row)) {      // keys that nobody sees
-            codes[i][0] = codes[i][1] = codes[i][2] = codes[i][3] = 0u;
-            byte[i] = 0;
+            codes[0] = codes[1] = codes[2] = codes[3] = 0u;
+            byte = 0;
           }
-          rare |= byte[i] > kE4m3FastByte || e4m3_any_nan<4>(codes[i]) != 0;
-        }
-        rare = __any_sync(0xffffffffu, rare);       // one branch for the warp and the tile
+        };
         auto put = [&](int i, const uint32_t (&y)[8]) {
           // chunks 2c and 2c + 1 of the row, 8 to a 64-column box
-          const int r = i * RPP + r_in, box = c >> 2, cc = (2 * c) & 7;
+          const int r = at(i), box = c >> 2, cc = (2 * c) & 7;
           uint8_t* row = out + box * C::kBox + r * 128;
           *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
         };
-        if (!rare) {
+        uint32_t codes[NP][4];
+        int byte[NP];
+        bool rare = false;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          load(i, codes[i], byte[i]);
+          rare |= byte[i] > kE4m3FastByte || e4m3_any_nan<4>(codes[i]) != 0;
+        }
+        if (!__any_sync(0xffffffffu, rare)) {       // one branch for the warp and the tile
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             uint32_t y[8];
@@ -575,10 +574,12 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
             put(i, y);
           }
         } else {
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < NP; ++i) {
-            uint32_t y[8];
-            e4m3_widen<4>(codes[i], byte[i], true, y);
+            uint32_t again[4], y[8];
+            int b;
+            load(i, again, b);
+            e4m3_widen<4>(again, b, true, y);
             put(i, y);
           }
         }
