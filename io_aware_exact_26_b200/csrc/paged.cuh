@@ -272,15 +272,6 @@ struct PagedWalk {
   }
 };
 
-// mbar_wait without a look at the clock for the first tries: the waits on a tile's path
-// mostly end within them.
-__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity);
-}
-
 // Pieces passed from the producer warp to the consumer warps, in order.
 struct SegRing {
   uint64_t full[4];           // count 1
@@ -296,7 +287,7 @@ __device__ __forceinline__ void seg_ring_init(SegRing& r, uint32_t consumers) {
 // Producer (one thread): post the k-th piece; false if a wait failed.
 __device__ __forceinline__ bool seg_ring_post(SegRing& r, int k, const PagedSeg& w) {
   const int i = k & 3;
-  if (k >= 4 && !pipe_wait(&r.empty[i], ((k >> 2) - 1) & 1)) return false;
+  if (k >= 4 && !mbar_wait(&r.empty[i], ((k >> 2) - 1) & 1)) return false;
   r.seg[i] = w;
   mbar_arrive(&r.full[i]);
   return true;
@@ -306,7 +297,7 @@ __device__ __forceinline__ PagedSeg seg_ring_take(SegRing& r, int k, int lane, b
   const int i = k & 3;
   PagedSeg w;
   w.n = 0;
-  ok = __all_sync(0xffffffffu, pipe_wait(&r.full[i], (k >> 2) & 1));
+  ok = __all_sync(0xffffffffu, mbar_wait(&r.full[i], (k >> 2) & 1));
   if (!ok) return w;
   w = r.seg[i];
   __syncwarp();
@@ -330,7 +321,7 @@ __device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddep
 // ------------------------------------------------------------------ pipeline shared by the kernels
 // Barriers between the producer warp, the widening warps (e4m3 cache) and the MMA warp.
 struct PagedPipe {
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[2], q_empty[2], q8_full[2];
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
   uint64_t raw_full[8], raw_empty[8];
   SegRing ring;
@@ -338,15 +329,20 @@ struct PagedPipe {
   PagedPlan plan;
   uint32_t tmem_base;
 };
+// C::KV8: the cache is e4m3.  C::K8: K tiles go to the tensor cores as e4m3 (Q then does as
+// well, in two parts); else the widening warps turn them into bf16 tiles like those of V.
 template <class C>
 __device__ __forceinline__ void paged_pipe_init(PagedPipe& sh, int ring_consumers, int warps) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&sh.q_full[i], 1);
     mbar_init(&sh.q_empty[i], 1);
+    mbar_init(&sh.q8_full[i], C::K8 ? C::kWiden : 1);
   }
-  for (int i = 0; i < C::KST; ++i) {
-    mbar_init(&sh.k_full[i], C::KV8 ? C::kWiden : 1);
+  for (int i = 0; i < C::KSK; ++i) {
+    mbar_init(&sh.k_full[i], C::KV8 && !C::K8 ? C::kWiden : 1);
     mbar_init(&sh.k_empty[i], 1);
+  }
+  for (int i = 0; i < C::KSV; ++i) {
     mbar_init(&sh.v_full[i], C::KV8 ? C::kWiden : 1);
     mbar_init(&sh.v_empty[i], 1);
   }
@@ -361,7 +357,9 @@ __device__ __forceinline__ void paged_pipe_init(PagedPipe& sh, int ring_consumer
 
 // Shared-memory regions of a kernel.
 struct PagedSmem {
-  uint8_t *q, *k, *v, *raw, *scale;
+  uint8_t *q, *k, *v;         // tiles as the tensor cores read them (q: bf16)
+  uint8_t *raw, *scale;       // e4m3 tiles before widening, 128 scale bytes per stage
+  uint8_t* kscale;            // K8: scale bytes of the last 8 K tiles
 };
 
 // Pages of a key tile that hold keys in [kmin, len): local indices.
@@ -426,7 +424,7 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
       ok = seg_ring_post(sh.ring, k, w);
       if (ok && w.n > 0) {
         const int qs = uq % C::QST;
-        if (uq >= C::QST) ok = pipe_wait(&sh.q_empty[qs], ((uq / C::QST) - 1) & 1);
+        if (uq >= C::QST) ok = mbar_wait(&sh.q_empty[qs], ((uq / C::QST) - 1) & 1);
         if (ok) {
           mbar_arrive_expect_tx(&sh.q_full[qs], p.G * p.R * C::D * 2);
           for (int c = 0; c < C::NB; ++c)
@@ -450,26 +448,37 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         uint64_t *full, *empty;
-        uint8_t* dst;
+        uint8_t *dst, *scale = nullptr;
         int st, round;                              // stage, and which use of it this is
-        if constexpr (C::KV8) {
-          const int rc = 2 * kc + kv;
-          st = rc % C::RST;
-          round = rc / C::RST;
+        // bytes per key that the copies bring in: a padded e4m3 row of 128 bytes for K8
+        constexpr int kRow8 = C::KV8 ? C::D : 2 * C::D;
+        const int row_bytes = kv == 0 && C::K8 ? 128 : kRow8;
+        if (C::KV8 && !(C::K8 && kv == 0)) {
+          const int rc = C::K8 ? kc : 2 * kc + kv;
+          st = rc % C::kRawMod;
+          round = rc / C::kRawMod;
           full = &sh.raw_full[st];
           empty = &sh.raw_empty[st];
           dst = m.raw + st * C::kRawTile;
+          scale = m.scale + st * 128;
+        } else if (kv == 0) {
+          st = kc % C::KSK;
+          round = kc / C::KSK;
+          full = &sh.k_full[st];
+          empty = &sh.k_empty[st];
+          dst = m.k + st * C::kKTile;
+          scale = m.kscale + (kc & 7) * 128;
         } else {
-          st = kc % C::KST;
-          round = kc / C::KST;
-          full = kv ? &sh.v_full[st] : &sh.k_full[st];
-          empty = kv ? &sh.v_empty[st] : &sh.k_empty[st];
-          dst = (kv ? m.v : m.k) + st * C::kTile;
+          st = kc % C::KSV;
+          round = kc / C::KSV;
+          full = &sh.v_full[st];
+          empty = &sh.v_empty[st];
+          dst = m.v + st * C::kTile;
         }
         if (lane == 0) {
-          if (round > 0) ok = pipe_wait(empty, (round - 1) & 1);
+          if (round > 0) ok = mbar_wait(empty, (round - 1) & 1);
           if (ok) {
-            if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * (C::KV8 ? C::D + 1 : 2 * C::D));
+            if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * (row_bytes + (C::KV8 ? 1 : 0)));
             else mbar_arrive(full);
           }
         }
@@ -479,10 +488,9 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
           const int r0 = (t.first + bx) << psh;     // row of the box in the tile
           in_range(r0 + rows - 1, 128);
           if constexpr (C::KV8) {
-            tma_load_4d(dst + r0 * C::D, kv ? tmv : tmk, full, 0, y, w.g, z);
+            tma_load_4d(dst + r0 * row_bytes, kv ? tmv : tmk, full, 0, y, w.g, z);
             const long long pg = page < 0 ? 0 : page;          // scale bytes of some page of the pool
-            bulk_load(m.scale + st * 128 + r0, (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y),
-                      rows, full);
+            bulk_load(scale + r0, (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y), rows, full);
           } else {
             tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? tmv : tmk, full, bc * 64, y, w.g, z);
           }
@@ -494,12 +502,16 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
     }
   }
   if (!ok && lane == 0) {                           // let copies in flight land
-    for (int r = max(0, nk - (C::KV8 ? C::RST : 2 * C::KST)); r < nk; ++r) {
-      if constexpr (C::KV8) {
-        mbar_drain_wait(&sh.raw_full[r % C::RST], (r / C::RST) & 1);
+    for (int r = max(0, nk - 16); r < nk; ++r) {    // at most 8 stages of each kind: older ones have landed
+      const int kt = r >> 1, kv = r & 1;
+      if (C::KV8 && !(C::K8 && kv == 0)) {
+        const int rc = C::K8 ? kt : r;
+        if (rc >= (C::K8 ? (nk + 1) / 2 : nk) - C::RST)
+          mbar_drain_wait(&sh.raw_full[rc % C::kRawMod], (rc / C::kRawMod) & 1);
+      } else if (kv == 0) {
+        if (kt >= (nk + 1) / 2 - C::KSK) mbar_drain_wait(&sh.k_full[kt % C::KSK], (kt / C::KSK) & 1);
       } else {
-        const int kt = r >> 1;
-        mbar_drain_wait((r & 1) ? &sh.v_full[kt % C::KST] : &sh.k_full[kt % C::KST], (kt / C::KST) & 1);
+        if (kt >= (nk + 1) / 2 - C::KSV) mbar_drain_wait(&sh.v_full[kt % C::KSV], (kt / C::KSV) & 1);
       }
     }
     for (int r = max(0, uq - C::QST); r < uq; ++r) mbar_drain_wait(&sh.q_full[r % C::QST], (r / C::QST) & 1);
@@ -507,15 +519,16 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
   __syncwarp();
 }
 
-// Widening warps (e4m3 cache), wt = 0 .. 32 kWiden - 1.  A lane takes 16 codes of a row,
+// Widening warps (e4m3 cache), wt = 0 .. 32 kWiden - 1; split_q(k, qs) readies Q of the k-th
+// piece in buffer qs (K8).  A lane takes 16 codes of a row,
 // widens them with the row's scale and stores two 16-byte chunks of the bf16 tile in the
 // 128B-swizzled layout the TMA would write.  Eight lanes (one shared-memory wavefront)
 // take 4 chunks of each of 2 rows: their stores then fall on 8 different chunk positions.
 // At d = 128 the raw tile is swizzled too, and lanes 0-7 take the chunks {0, 5, 2, 7},
 // lanes 8-15 {1, 4, 3, 6} of their rows, for which the loads of both rows are disjoint as
 // well (without this, 30% more time per tile).
-template <class C>
-__device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, int wt, int lane) {
+template <class C, typename SplitQ>
+__device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, int wt, int lane, SplitQ split_q) {
   constexpr int D = C::D;
   constexpr int CPR = D / 16;                       // 16-code chunks per row
   constexpr int RPP = 32 * C::kWiden / CPR;         // rows per pass
@@ -527,15 +540,25 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
   for (int k = 0; ok; ++k) {
     const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
     if (w.n == 0) break;
+    if constexpr (C::K8) {
+      const int qs = k % C::QST;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.q_full[qs], (k / C::QST) & 1));
+      if (!ok) break;
+      split_q(k, qs);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q8_full[qs]);
+    }
     for (int j = 0; j < w.n && ok; ++j, ++kc) {
       const int lo = w.kmin - (w.j0 + j) * 128, hi_row = w.len - (w.j0 + j) * 128;
-      const int st = kc % C::KST;
+      static_assert(C::K8 || C::KSK == C::KSV, "K and V tiles are widened in turn");
+      const int st = kc % C::KSV;
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        const int rc = 2 * kc + kv, rs = rc % C::RST;
-        ok = __all_sync(0xffffffffu, pipe_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
-        if (ok && kc >= C::KST)
-          ok = __all_sync(0xffffffffu, pipe_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], ((kc / C::KST) - 1) & 1));
+      for (int kv = C::K8 ? 1 : 0; kv < 2; ++kv) {
+        const int rc = C::K8 ? kc : 2 * kc + kv, rs = rc % C::RST;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
+        if (ok && kc >= C::KSV)
+          ok = __all_sync(0xffffffffu, mbar_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], ((kc / C::KSV) - 1) & 1));
         if (!ok) break;
         const uint8_t* raw = m.raw + rs * C::kRawTile;
         uint8_t* out = (kv ? m.v : m.k) + st * C::kTile;

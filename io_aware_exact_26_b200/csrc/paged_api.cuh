@@ -103,7 +103,9 @@ void launch_cache_read(const attn::ReadParams& p, int B, cudaStream_t s) {
 // [num_pages][Hkv][page_size][d] as a 4-D map; one box is a page's (or 128 rows of it)
 // 64 bf16 columns, swizzled as the MMAs read them, or all e4m3 columns (swizzled at d = 128,
 // where a row is one 128-byte line, so that the widening warps read without conflicts).
-bool make_cache_map(CUtensorMap* m, const void* ptr, const attn_cache_t* c) {
+// `pad`: e4m3 boxes of 128 columns whatever d is (zeros behind the row), swizzled, as the
+// tensor cores read 8-bit tiles.
+bool make_cache_map(CUtensorMap* m, const void* ptr, const attn_cache_t* c, bool pad = false) {
   auto enc = encode_fn();
   if (!enc) return false;
   const int elem = c->dtype == ATTN_BF16 ? 2 : 1;
@@ -111,12 +113,12 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, const attn_cache_t* c) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page_size),
                         static_cast<cuuint64_t>(c->Hkv), static_cast<cuuint64_t>(c->num_pages)};
   cuuint64_t strides[3] = {row, row * c->page_size, static_cast<cuuint64_t>(c->page_stride) * elem};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(elem == 2 ? 64 : c->d),
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(elem == 2 ? 64 : pad ? 128 : c->d),
                        static_cast<cuuint32_t>(c->page_size < 128 ? c->page_size : 128), 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
              const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             row >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             row >= 128 || pad ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -195,7 +197,7 @@ int launch_paged(Kernel kernel, const void* q, const attn_strides_t* q_strides, 
   });
   if (!attr_ok[dev]) return ATTN_ERR_LAUNCH;
   CUtensorMap tq, tk, tv;
-  if (!make_q_map(&tq, q, q_strides, p.T, p.Hq, cache->d, p.G, p.R) || !make_cache_map(&tk, cache->k, cache) ||
+  if (!make_q_map(&tq, q, q_strides, p.T, p.Hq, cache->d, p.G, p.R) || !make_cache_map(&tk, cache->k, cache, C::K8) ||
       !make_cache_map(&tv, cache->v, cache))
     return ATTN_ERR_LAUNCH;
   if (launch_pdl(kernel, dim3(p.ctas), C::kThreads, C::kSmem, stream, tq, tk, tv, p) != cudaSuccess)

@@ -13,13 +13,26 @@
 // 2^kRescaleTau; only then (the first tiles of an item) are the maxima reduced, the base
 // raised and O and the sums rescaled.  The sums stay per thread until the item ends.
 //
-//   warps 0-3   softmax (thread = key of the tile = TMEM lane; in the epilogue = column of O)
-//   warp 4      producer (paged_produce)
-//   warp 5      MMA issuer: S up to 3 tiles ahead (4 buffers of NQ columns), P double-buffered
-//   warps 6-13  widening warps (e4m3 cache)
+// A tile's chain (scores, vote, exponentials, P, fence) is latency, not work: two groups of
+// softmax warps take alternate tiles, each with its own bases, sums and O, joined like two
+// shares of the keys when the item ends.
+//
+//   warps 0-3, 4-7  softmax groups 0, 1: group g % 2 takes step g (thread = key of the tile =
+//                   TMEM lane); the epilogue is group 0's (thread = column of O)
+//   warp 8          producer (paged_produce)
+//   warp 9          MMA issuer: S runs SA steps ahead in 4 buffers of NQ columns
+//   warps 10-       widening warps (e4m3 cache)
 // P goes through shared memory (K-major, 128B swizzle) as the second operand of O^T; V is
 // read column-major as the first.  At d = 64 the 128 rows of O^T hold d in the first 64;
 // the others come from the 16 KB behind the V tile and are never read.
+//
+// e4m3 cache.  K goes to the tensor cores as it lies (no widening: half of that work and of
+// its shared-memory traffic), so Q has to be 8-bit too, without losing anything: a bf16
+// value has 8 significant bits, e4m3 has 4, and q 2^-e = hi + lo with hi its nearest e4m3
+// and lo the rest.  With e from the row's largest magnitude (at most 448 2^e) the sum is
+// exact for values down to 2^-10 of it and off by at most 2^-18 of it below.  S = hi K +
+// lo K; the scales 2^e of a query row and of a key multiply the scores in the softmax
+// threads (a thread has one key).  V is widened to bf16, as its products with P need.
 #pragma once
 #include "paged.cuh"
 
@@ -28,32 +41,43 @@ namespace attn {
 template <int D_, bool KV8_, int NQ>
 struct FewCfg {
   static constexpr int D = D_;
-  static constexpr bool KV8 = KV8_;
-  static constexpr int kTile = 128 * D * 2;
+  static constexpr bool KV8 = KV8_, K8 = KV8_;
+  static constexpr int kTile = 128 * D * 2;        // bf16 tile
   static constexpr int kBox = 128 * 128;
   static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
+  static constexpr int kKTile = K8 ? 128 * 128 : kTile;
   static constexpr int kQBox = NQ * 128;
   static constexpr int kQTile = NB * kQBox;
   static constexpr int kPTile = 2 * kQBox;         // P^T: NQ rows of 128 keys
   static constexpr int QST = (NQ == 32 && D == 128 && !KV8) ? 1 : 2;
-  static constexpr int KST = KV8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);   // stages of K, and of V
-  static constexpr int SA = KST < 3 ? KST : 3;     // tiles that S runs ahead
-  static constexpr int kWiden = KV8 ? 8 : 0;
-  static constexpr int kThreads = 192 + 32 * kWiden;
+  static constexpr int kQ8 = K8 ? 2 * kQBox : 0;   // hi and lo parts of Q, 128-byte rows
+  static constexpr int KSK = K8 ? (NQ == 32 && D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
+  static constexpr int KSV = KV8 ? (D == 128 ? 2 : 3) : KSK;
+  // S(g) completes behind PV(g - SA), so P(g) may take the buffer of P(g - NP) for NP >= SA
+  static constexpr int SA = NQ == 16 ? 3 : 2;
+  static constexpr int NP = NQ == 16 ? 4 : 2;
+  static_assert(SA <= KSK && SA <= KSV + 1 && NP >= SA && (!K8 || KSK + SA + 1 <= 8), "stages");
+  static constexpr int kWiden = KV8 ? (NQ == 16 ? 8 : 4) : 0;
+  static constexpr int kThreads = 320 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;
-  static constexpr int kRoom = 232448 - 1024 - 2 * KST * kTile - QST * kQTile - 2 * kPTile - 3072;
+  static constexpr int kShared = NQ == 16 ? 4096 : 6144;
+  static constexpr int kRoom = 232448 - 1024 - KSK * kKTile - KSV * kTile - QST * (kQTile + kQ8) - NP * kPTile -
+                               1024 - kShared;
   static constexpr int kRawFit = kRoom / (kRawTile + 128);
   static constexpr int RST = KV8 ? (kRawFit < 8 ? kRawFit : 8) : 0;   // as many raw stages as fit: bytes in flight
-  static constexpr int kO = 4 * NQ;                // TMEM: S buffers at 0, NQ, 2 NQ, 3 NQ, then O
+  static constexpr int kRawMod = KV8 ? RST : 1;
+  static constexpr int kO = 4 * NQ;                // TMEM: S buffers at 0, NQ, 2 NQ, 3 NQ, then O of each group
   static constexpr int kTmemCols = NQ == 16 ? 128 : 256;
   static constexpr int kOffK = 0;
-  static constexpr int kOffV = KST * kTile;
-  static constexpr int kOffRaw = kOffV + KST * kTile;
+  static constexpr int kOffV = KSK * kKTile;
+  static constexpr int kOffRaw = kOffV + KSV * kTile;
   static constexpr int kOffQ = kOffRaw + RST * kRawTile;
-  static constexpr int kOffP = kOffQ + QST * kQTile;
-  static constexpr int kOffScale = kOffP + 2 * kPTile;
-  static constexpr int kOffSh = kOffScale + RST * 128;
-  static constexpr int kEnd = kOffSh + 3072;
+  static constexpr int kOffQ8 = kOffQ + QST * kQTile;
+  static constexpr int kOffP = kOffQ8 + QST * kQ8;
+  static constexpr int kOffScale = kOffP + NP * kPTile;
+  static constexpr int kOffKScale = kOffScale + RST * 128;
+  static constexpr int kOffSh = kOffKScale + 1024;
+  static constexpr int kEnd = kOffSh + kShared;
   static constexpr int kLayout = kEnd > kOffRaw + kBox ? kEnd : kOffRaw + kBox;   // d = 64 reads 16 KB behind V
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 232448, "shared memory layout exceeds 227 KB");
@@ -62,18 +86,23 @@ struct FewCfg {
 
 template <int NQ>
 struct FewShared : PagedPipe {
-  float wmax[4][NQ], wsum[4][NQ];      // per softmax warp
-  int vote[2][4];                      // [step parity][warp]
-  uint64_t s_full[4];
-  uint64_t p_ready[2], pv_done[2];     // [step parity]
-  uint64_t vbar[2];                    // [step parity]: the four warps voted
-  uint64_t xbar, sbar;                 // the four warps posted their maxima / their sums
+  float wmax[2][4][NQ];                // [group][warp]
+  float wsum[2][2][4][NQ];             // [piece parity][group][warp]
+  float base[2][2][NQ];                // [piece parity][group] exponent bases
+  float cq[4][NQ];                     // K8: 2^e of the query rows, by piece % 4
+  int vote[2][2][4];                   // [group][parity of its steps][warp]
+  // By step % 4: S runs up to 3 steps ahead of P V, so a group may finish two of its steps
+  // before the MMA warp looks at the first (a parity wait tells two successive phases apart).
+  uint64_t s_full[4], p_ready[4], pv_done[4];
+  uint64_t vbar[2][2];                 // [group][parity of its steps]: its four warps voted
+  uint64_t xbar[2];                    // [group]: its four warps posted their maxima
+  uint64_t done[2];                    // [piece parity]: all eight warps posted sums and bases
   uint64_t o_free;
 };
 
 // Reduction over the 32 lanes of NQ values per lane: each halving step exchanges half of
 // the values still held, so it takes NQ - 1 (+ 1) shuffles instead of 5 NQ.  Afterwards
-// v[0] holds the result of value `few_owner`.
+// v[0] holds the result of value few_owner(lane).
 template <int NQ, typename Op>
 __device__ __forceinline__ float few_reduce(float (&v)[NQ], int lane, Op op) {
 #pragma unroll
@@ -112,30 +141,81 @@ __device__ __forceinline__ void few_tmem_ld(uint32_t addr, float (&f)[NQ]) {
   }
 }
 
+// 2^(byte - 127), also for byte 0 (subnormal).
+__device__ __forceinline__ float e8m0_value(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
+
+// Q of a piece as hi + lo parts (see the head of this file), row scales to cq.
+template <class C, int NQ>
+__device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float* cq, int wt) {
+  constexpr int CPR = C::D / 8;                      // 8-value chunks per row, one per lane
+  for (int x = wt; x < NQ * CPR; x += 32 * C::kWiden) {
+    const int r = x / CPR, c = x % CPR;
+    const uint4 raw = *reinterpret_cast<const uint4*>(q + (c >> 3) * C::kQBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    float f[8];
+    Vec16<__nv_bfloat16>::load(raw, f);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(f[i]);
+      amax = fmaxf(amax, a < INFINITY ? a : 0.f);
+    }
+#pragma unroll
+    for (int m = CPR / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    const int e = e4m3_exponent(amax);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[2], v[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float a = f[4 * h + 2 * k] * inv, b = f[4 * h + 2 * k + 1] * inv;
+        if (!(fabsf(a) < INFINITY)) a = NAN;         // an infinite query value gives no finite score
+        if (!(fabsf(b) < INFINITY)) b = NAN;
+        w[k] = pack_e4m3x2(a, b);
+        const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[k]), __NV_E4M3);
+        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        v[k] = pack_e4m3x2(a - g.x, b - g.y);
+      }
+      hi[h] = w[0] | (w[1] << 16);
+      lo[h] = v[0] | (v[1] << 16);
+    }
+    const int off = r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+    *reinterpret_cast<uint2*>(q8 + off) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(q8 + C::kQBox + off) = make_uint2(lo[0], lo[1]);
+    if (c == 0) cq[r] = e8m0_value(static_cast<uint32_t>(e + 127));
+  }
+}
+
 template <int D, bool KV8, int NQ>
 __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
     attn_paged_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const PagedParams p) {
   using C = FewCfg<D, KV8, NQ>;
-  static_assert(sizeof(FewShared<NQ>) <= 3072, "FewShared does not fit its slot");
+  static_assert(sizeof(FewShared<NQ>) <= C::kShared, "FewShared does not fit its slot");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FewShared<NQ>& sh = *reinterpret_cast<FewShared<NQ>*>(smem + C::kOffSh);
-  const PagedSmem m = {smem + C::kOffQ, smem + C::kOffK, smem + C::kOffV, smem + C::kOffRaw, smem + C::kOffScale};
+  const PagedSmem m = {smem + C::kOffQ,   smem + C::kOffK,     smem + C::kOffV,
+                       smem + C::kOffRaw, smem + C::kOffScale, smem + C::kOffKScale};
+  uint8_t* sQ8 = smem + C::kOffQ8;
   uint8_t* sP = smem + C::kOffP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    paged_pipe_init<C>(sh, 5 + C::kWiden, 6 + C::kWiden);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.s_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.p_ready[i], 4);
+    paged_pipe_init<C>(sh, 9 + C::kWiden, 10 + C::kWiden);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.vbar[i], 4);
+      mbar_init(&sh.p_ready[i], 4);
     }
-    mbar_init(&sh.xbar, 4);
-    mbar_init(&sh.sbar, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.vbar[i][0], 4);
+      mbar_init(&sh.vbar[i][1], 4);
+      mbar_init(&sh.xbar[i], 4);
+      mbar_init(&sh.done[i], 8);
+    }
     mbar_init(&sh.o_free, 4);
     fence_barrier_init();
   }
@@ -148,36 +228,47 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
-  if (warp == 4) {
+  if (warp == 8) {
     paged_produce<C>(p, sh, &tmq, &tmk, &tmv, m, cta, lane);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
-    constexpr uint32_t idS = idesc_bf16_f32(128, NQ, false, false);
+    constexpr uint32_t idS = KV8 ? idesc_e4m3_f32(128, NQ, false, false) : idesc_bf16_f32(128, NQ, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(128, NQ, true, false);
     constexpr uint32_t hi = sdesc_hi_sw128(1024);
-    const uint32_t q_lo0 = sdesc_lo(smem_u32(m.q), 16);
+    const uint32_t q_lo0 = sdesc_lo(smem_u32(KV8 ? sQ8 : m.q), 16);
     const uint32_t k_lo0 = sdesc_lo(smem_u32(m.k), 16);
     const uint32_t v_lo0 = sdesc_lo(smem_u32(m.v), C::kBox);
     const uint32_t p_lo0 = sdesc_lo(smem_u32(sP), 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, pipe_wait(bar, parity));
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
     int kc = 0, vc = 0, gs = 0, uq = 0;
     bool ok = true;
-    // S^T(g) = K(kc) Q^T into buffer g % 4.  Its last reader arrived on p_ready(g - 4),
-    // which PV(g - 4), issued before, waited for.
+    // S^T(g) = K(kc) Q^T into buffer g % 4.  Its last reader arrived on p_ready for step
+    // g - 4, which PV(g - 4), issued before, waited for.
     auto issue_s = [&](int g, int qs, bool last) -> bool {
-      const int st = kc % C::KST;
-      if (!wait(&sh.k_full[st], (kc / C::KST) & 1)) return false;
+      const int st = kc % C::KSK;
+      if (!wait(&sh.k_full[st], (kc / C::KSK) & 1)) return false;
       tc_fence_after();
       if (leader) {
-        const uint32_t q_lo = q_lo0 + qs * (C::kQTile >> 4);
-        const uint32_t k_lo = k_lo0 + st * (C::kTile >> 4);
+        const uint32_t k_lo = k_lo0 + st * (C::kKTile >> 4);
+        const uint32_t d = tmem + (g & 3) * NQ;
+        if constexpr (KV8) {
+          const uint32_t q_lo = q_lo0 + qs * (C::kQ8 >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_ss_lo(tmem + (g & 3) * NQ, k_lo + (((k >> 2) * C::kBox + (k & 3) * 32) >> 4),
-                     q_lo + (((k >> 2) * C::kQBox + (k & 3) * 32) >> 4), hi, idS, k > 0);
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              umma_ss_f8_lo(d, k_lo + ((k * 32) >> 4), q_lo + ((part * C::kQBox + k * 32) >> 4), hi, idS,
+                            part + k > 0);
+        } else {
+          const uint32_t q_lo = q_lo0 + qs * (C::kQTile >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            umma_ss_lo(d, k_lo + (((k >> 2) * C::kBox + (k & 3) * 32) >> 4),
+                       q_lo + (((k >> 2) * C::kQBox + (k & 3) * 32) >> 4), hi, idS, k > 0);
+        }
         umma_commit(&sh.s_full[g & 3]);
         umma_commit(&sh.k_empty[st]);
         if (last) umma_commit(&sh.q_empty[qs]);
@@ -190,24 +281,24 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
       const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
       if (w.n == 0) break;
       const int qs = uq % C::QST;
-      ok = wait(&sh.q_full[qs], (uq / C::QST) & 1);
+      ok = wait(KV8 ? &sh.q8_full[qs] : &sh.q_full[qs], (uq / C::QST) & 1);
       for (int t = 0; t < C::SA && t < w.n && ok; ++t) ok = issue_s(gs + t, qs, t == w.n - 1);
       for (int j = 0; j < w.n && ok; ++j, ++vc) {
-        const int g = gs + j, vst = vc % C::KST;
-        ok = wait(&sh.v_full[vst], (vc / C::KST) & 1);
+        const int g = gs + j, vst = vc % C::KSV;
+        ok = wait(&sh.v_full[vst], (vc / C::KSV) & 1);
         if (!KV8 && ok) paged_zero_v<C>(w, j, m.v + vst * C::kTile, lane);
-        if (ok) ok = wait(&sh.p_ready[g & 1], (g >> 1) & 1);
+        if (ok) ok = wait(&sh.p_ready[g & 3], (g >> 2) & 1);
         if (ok && j == 0 && uq >= 1) ok = wait(&sh.o_free, (uq - 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
           const uint32_t v_lo = v_lo0 + vst * (C::kTile >> 4);
-          const uint32_t p_lo = p_lo0 + (g & 1) * (C::kPTile >> 4);
+          const uint32_t p_lo = p_lo0 + (g % C::NP) * (C::kPTile >> 4);
 #pragma unroll
           for (int k2 = 0; k2 < 8; ++k2)
-            umma_ss_lo(tmem + C::kO, v_lo + ((k2 * 2048) >> 4), p_lo + (((k2 >> 2) * C::kQBox + (k2 & 3) * 32) >> 4),
-                       hi, idO, !(j == 0 && k2 == 0));
-          umma_commit(&sh.pv_done[g & 1]);
+            umma_ss_lo(tmem + C::kO + (g & 1) * NQ, v_lo + ((k2 * 2048) >> 4),
+                       p_lo + (((k2 >> 2) * C::kQBox + (k2 & 3) * 32) >> 4), hi, idO, !(j < 2 && k2 == 0));
+          umma_commit(&sh.pv_done[g & 3]);
           umma_commit(&sh.v_empty[vst]);
         }
         __syncwarp();
@@ -221,45 +312,56 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
       mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 6) {
-    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 192, lane);
+  } else if (warp >= 10) {
+    if constexpr (KV8) {
+      const int wt = threadIdx.x - 320;
+      paged_widen<C>(sh, m, wt, lane, [&](int k, int qs) {
+        few_split_q<C, NQ>(m.q + qs * C::kQTile, sQ8 + qs * C::kQ8, sh.cq[k & 3], wt);
+      });
+    }
   } else {
-    // ------------------------------------------------------------ softmax warps 0-3
-    const int row = warp * 32 + lane;                           // key of the tile, column of O
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const bool has_o = warp * 32 < D;                           // d = 64: warps 0 and 1 hold O
-    const float c = p.cs;
+    // ------------------------------------------------------------ softmax groups
+    const int x2 = warp >> 2, wq = warp & 3;                    // group, warp of the group
+    const int row = wq * 32 + lane;                             // key of the tile, column of O
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const bool has_o = wq * 32 < D;                             // d = 64: the first two warps hold O
     uint8_t* prow = sP + (row >> 6) * C::kQBox + (row & 7) * 2;
     const int chunk = ((row & 63) >> 3) << 4;
     int gs = 0, uq = 0, fs = 0;                                 // steps, pieces, raised bases
     bool ok = true;
-    auto all_warps = [&](uint64_t* bar, uint32_t parity) -> bool {
+    auto group_sync = [&](uint64_t* bar, uint32_t parity) -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
-      return __all_sync(0xffffffffu, pipe_wait(bar, parity));
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
     for (int k = 0; ok; ++k) {
       const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
       if (w.n == 0) break;
       const int nrows = w.ntok * p.G;                           // rows 0 .. nrows - 1 are real
-      const int pos_last = w.pos0 + w.ntok - 1;
       // keys [all_lo, all_hi] are visible to every row
       const int all_hi = p.causal ? min(w.len - 1, w.pos0) : w.len - 1;
-      const int all_lo = p.wl >= 0 ? pos_last - p.wl : 0;
+      const int all_lo = p.wl >= 0 ? w.pos0 + w.ntok - 1 - p.wl : 0;
       float mu[NQ], ls[NQ];
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         mu[q] = -INFINITY;
         ls[q] = 0.f;
       }
-      for (int j = 0; j < w.n; ++j) {
-        const int g = gs + j, par = g & 1;
-        ok = __all_sync(0xffffffffu, pipe_wait(&sh.s_full[g & 3], (g >> 2) & 1));
+      const int g_end = gs + w.n;
+      for (int g = gs + ((gs ^ x2) & 1); g < g_end; g += 2) {
+        const int par = (g >> 1) & 1;                           // parity of the group's steps
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g & 3], (g >> 2) & 1));
         if (!ok) break;
         tc_fence_after();
         float x[NQ];
         few_tmem_ld<NQ>(lane_base + (g & 3) * NQ, x);
-        const int k0 = (w.j0 + j) * 128, key = k0 + row;
+        float c = p.cs;
+        if constexpr (KV8) {
+          c *= e8m0_value(m.kscale[(g & 7) * 128 + row]);       // this key's scale
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) x[q] *= sh.cq[uq & 3][q];
+        }
+        const int k0 = (w.j0 + g - gs) * 128, key = k0 + row;
         bool up = false;
         if (k0 >= all_lo && k0 + 127 <= all_hi) {
 #pragma unroll
@@ -279,52 +381,54 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
           }
         }
         up = __any_sync(0xffffffffu, up);
-        if (lane == 0) sh.vote[par][warp] = up;
-        ok = all_warps(&sh.vbar[par], (g >> 1) & 1);
+        if (lane == 0) sh.vote[x2][par][wq] = up;
+        ok = group_sync(&sh.vbar[x2][par], (g >> 2) & 1);
         if (!ok) break;
-        const volatile int* votes = sh.vote[par];
+        const volatile int* votes = sh.vote[x2][par];
         if (votes[0] | votes[1] | votes[2] | votes[3]) {
-          float t[NQ];
+          {
+            float t[NQ];
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) t[q] = x[q];
-          sh.wmax[warp][few_owner<NQ>(lane)] = few_reduce<NQ>(t, lane, [](float a, float b) { return fmaxf(a, b); });
-          ok = all_warps(&sh.xbar, fs & 1);
+            for (int q = 0; q < NQ; ++q) t[q] = x[q];
+            sh.wmax[x2][wq][few_owner<NQ>(lane)] =
+                few_reduce<NQ>(t, lane, [](float a, float b) { return fmaxf(a, b); });
+          }
+          ok = group_sync(&sh.xbar[x2], fs & 1);
           if (!ok) break;
           ++fs;
-          float alpha[NQ];
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const float top = fmaxf(fmaxf(sh.wmax[0][q], sh.wmax[1][q]), fmaxf(sh.wmax[2][q], sh.wmax[3][q]));
-            alpha[q] = 1.f;
-            if (top > mu[q]) {
-              alpha[q] = mu[q] == -INFINITY ? 0.f : ex2_approx(mu[q] - top);
-              mu[q] = top;
-              ls[q] *= alpha[q];
-            }
-          }
-          if (j > 0 && has_o) {                                 // O holds the steps before this one
-            ok = __all_sync(0xffffffffu, pipe_wait(&sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1));
+          const bool again = g - 2 >= gs && has_o;              // O holds the group's steps before this one
+          if (again) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g - 2) & 3], ((g - 2) >> 2) & 1));
             if (!ok) break;
             tc_fence_after();
-            float o[NQ];
-            few_tmem_ld<NQ>(lane_base + C::kO, o);
-#pragma unroll
-            for (int b = 0; b < NQ / 16; ++b) {
-              uint32_t r[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                r[i] = alpha[b * 16 + i] == 0.f ? 0u : __float_as_uint(o[b * 16 + i] * alpha[b * 16 + i]);
-              tmem_st16(lane_base + C::kO + b * 16, r);
-            }
-            tmem_wait_st();
           }
+#pragma unroll
+          for (int b = 0; b < NQ / 16; ++b) {
+            uint32_t o[16];
+            if (again) {
+              tmem_ld16(lane_base + C::kO + x2 * NQ + b * 16, o);
+              tmem_wait_ld();
+              reg_fence(o);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int q = b * 16 + i;
+              const float (&wm)[4][NQ] = sh.wmax[x2];
+              const float top = fmaxf(fmaxf(wm[0][q], wm[1][q]), fmaxf(wm[2][q], wm[3][q]));
+              float alpha = 1.f;
+              if (top > mu[q]) {
+                alpha = mu[q] == -INFINITY ? 0.f : ex2_approx(mu[q] - top);
+                mu[q] = top;
+                ls[q] *= alpha;
+              }
+              if (again) o[i] = alpha == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * alpha);
+            }
+            if (again) tmem_st16(lane_base + C::kO + x2 * NQ + b * 16, o);
+          }
+          if (again) tmem_wait_st();
         }
-        // P(g) goes where P(g - 2) was: PV(g - 2) has to be done
-        if (g >= 2) {
-          ok = __all_sync(0xffffffffu, pipe_wait(&sh.pv_done[par], ((g >> 1) - 1) & 1));
-          if (!ok) break;
-        }
-        uint8_t* dst = prow + par * C::kPTile;
+        // P(g) takes the buffer of P(g - NP): PV(g - NP) is done, S(g) came behind it
+        uint8_t* dst = prow + (g % C::NP) * C::kPTile;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           if (q < nrows) {
@@ -336,23 +440,41 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[par]);
+        if (lane == 0) mbar_arrive(&sh.p_ready[g & 3]);
       }
       if (!ok) break;
-      // epilogue: sums over the keys, the last PV, O / l and the LSE of this piece
-      const int glast = gs + w.n - 1;
+      // the group's sums over the keys and its bases.  Group 1 posts them only when group 0 has
+      // read O of the piece before: a group without a step in a piece would else run ahead of
+      // the buffers (and of the barrier) here.
+      const int pp = uq & 1;
+      if (x2 == 1 && uq >= 1) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.o_free, (uq - 1) & 1));
+        if (!ok) break;
+      }
       {
         float t[NQ];
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) t[q] = ls[q];
-        sh.wsum[warp][few_owner<NQ>(lane)] = few_reduce<NQ>(t, lane, [](float a, float b) { return a + b; });
+        for (int q = 0; q < NQ; ++q) {
+          t[q] = ls[q];
+          if (wq == 0 && lane == 0) sh.base[pp][x2][q] = mu[q];
+        }
+        sh.wsum[pp][x2][wq][few_owner<NQ>(lane)] = few_reduce<NQ>(t, lane, [](float a, float b) { return a + b; });
       }
-      ok = all_warps(&sh.sbar, uq & 1);
-      if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.done[pp]);
+      gs = g_end;
+      if (x2 == 1) { ++uq; continue; }
+      // epilogue (group 0): both groups' sums, the last PV, then O / l and the LSE of the piece
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.done[pp], (uq >> 1) & 1));
+      const int glast = g_end - 1;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 3], (glast >> 2) & 1));
       if (!ok) break;
       tc_fence_after();
-      float o[NQ];
-      few_tmem_ld<NQ>(lane_base + C::kO, o);
+      float o0[NQ], o1[NQ];
+      if (has_o) {
+        few_tmem_ld<NQ>(lane_base + C::kO, o0);
+        few_tmem_ld<NQ>(lane_base + C::kO + NQ, o1);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free);
@@ -360,25 +482,28 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (q < nrows) {
-          const float l = (sh.wsum[0][q] + sh.wsum[1][q]) + (sh.wsum[2][q] + sh.wsum[3][q]);
+          const float m0 = sh.base[pp][0][q], m1 = sh.base[pp][1][q], top = fmaxf(m0, m1);
+          const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - top), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - top);
+          const float (&s0)[4][NQ] = sh.wsum[pp][0], (&s1)[4][NQ] = sh.wsum[pp][1];
+          const float l = ((s0[0][q] + s0[1][q]) + (s0[2][q] + s0[3][q])) * f0 +
+                          ((s1[0][q] + s1[1][q]) + (s1[2][q] + s1[3][q])) * f1;
           const bool none = l == 0.f;                           // no key seen
-          const float val = none ? 0.f : o[q] * (1.f / l);
+          const float val = none ? 0.f : ((f0 == 0.f ? 0.f : o0[q] * f0) + (f1 == 0.f ? 0.f : o1[q] * f1)) * (1.f / l);
           const size_t orow = static_cast<size_t>(w.tok0 + i) * p.Hq + w.g * p.G + h;
           const bool store = in_range(w.tok0 + i, p.T) && in_range(q, w.slot < 0 ? NQ : p.slot_rows);
-          const size_t prow_ = static_cast<size_t>(w.slot < 0 ? 0 : w.slot) * p.slot_rows + q;
+          const size_t part = static_cast<size_t>(w.slot < 0 ? 0 : w.slot) * p.slot_rows + q;
           if (store && has_o) {
             if (w.slot < 0) p.o[orow * D + row] = __float2bfloat16_rn(val);
-            else p.opart[prow_ * D + row] = val;
+            else p.opart[part * D + row] = val;
           }
           if (store && row == q) {
-            const float lse = none ? -INFINITY : (mu[q] + __log2f(l)) * 0.69314718055994531f;
+            const float lse = none ? -INFINITY : (top + __log2f(l)) * 0.69314718055994531f;
             if (w.slot < 0) p.lse[orow] = lse;
-            else p.lpart[prow_] = lse;
+            else p.lpart[part] = lse;
           }
           if (++h == p.G) { h = 0; ++i; }
         }
       }
-      gs += w.n;
       ++uq;
     }
   }

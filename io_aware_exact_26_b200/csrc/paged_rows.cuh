@@ -17,18 +17,21 @@ struct RowsCfg {
   static constexpr int kBox = 128 * 128;
   static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
   static constexpr int QST = (KV8 && D == 128) ? 1 : 2;
-  static constexpr int KST = 2;                    // stages of K, and of V
+  static constexpr bool K8 = false;
+  static constexpr int KSK = 2, KSV = 2;           // stages of K and of V
+  static constexpr int kKTile = kTile;
   static constexpr int kQTile = kTile, kQBox = kBox;
   static constexpr int kWiden = KV8 ? 8 : 0;       // widening warps
   static constexpr int kThreads = 320 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
   static constexpr int RST = KV8 ? (D == 128 ? 3 : 6) : 0;   // raw stages, K and V tiles alternating
+  static constexpr int kRawMod = KV8 ? RST : 1;
   static constexpr int kS0 = 0, kS1 = 128, kO = 256;
   static constexpr int kTmemCols = 512;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = QST * kTile;
-  static constexpr int kOffV = kOffK + KST * kTile;
-  static constexpr int kOffRaw = kOffV + KST * kTile;
+  static constexpr int kOffV = kOffK + KSK * kTile;
+  static constexpr int kOffRaw = kOffV + KSK * kTile;
   static constexpr int kOffScale = kOffRaw + RST * kRawTile;  // 128 scale bytes per raw stage
   static constexpr int kOffSh = kOffScale + RST * 128;
   static constexpr int kLayout = kOffSh + 5120;
@@ -55,7 +58,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   RowsShared& sh = *reinterpret_cast<RowsShared*>(smem + C::kOffSh);
-  const PagedSmem m = {smem + C::kOffQ, smem + C::kOffK, smem + C::kOffV, smem + C::kOffRaw, smem + C::kOffScale};
+  const PagedSmem m = {smem + C::kOffQ, smem + C::kOffK, smem + C::kOffV, smem + C::kOffRaw, smem + C::kOffScale, nullptr};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
     const uint32_t k_lo0 = sdesc_lo(smem_u32(m.k), 16);
     const uint32_t v_lo0 = sdesc_lo(smem_u32(m.v), C::kBox);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, pipe_wait(bar, parity));
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
     int kc = 0, vc = 0, gs = 0, uq = 0;
     bool ok = true;
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 10) {
-    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 320, lane);
+    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 320, lane, [](int, int) {});
   } else {
     // ------------------------------------------------------------ softmax warps 0-7
     const int grp = warp >> 2;                                  // keys [64 grp, 64 grp + 64)
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       for (int j = 0; j < w.n && ok; ++j) {
         const int g2 = gs + j, xp = xs & 1;
         const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 64;
-        ok = __all_sync(0xffffffffu, pipe_wait(&sh.s_full[g2 & 1], (g2 >> 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g2 & 1], (g2 >> 1) & 1));
         if (!ok) break;
         if (!active) {
           if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
         sh.xmax[xp][grp][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.xbar[xp][quad]);
-        ok = __all_sync(0xffffffffu, pipe_wait(&sh.xbar[xp][quad], (xs >> 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[xp][quad], (xs >> 1) & 1));
         if (!ok) break;
         ++xs;
         const float mx = fmaxf(sh.xmax[xp][0][row], sh.xmax[xp][1][row]);
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
         // S(j) was issued before PV(j - 1) (and after PV(j - 2), which its commit covers):
         // wait for PV(j - 1) before rescaling O
         if (__any_sync(0xffffffffu, need && j > 0)) {
-          ok = __all_sync(0xffffffffu, pipe_wait(&sh.pv_done[(g2 - 1) & 1], ((g2 - 1) >> 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g2 - 1) & 1], ((g2 - 1) >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -303,12 +306,12 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sbar[quad]);
-      ok = __all_sync(0xffffffffu, pipe_wait(&sh.sbar[quad], uq & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar[quad], uq & 1));
       if (!ok) break;
       if (active) l = sh.xsum[0][row] + sh.xsum[1][row];
       // PV(glast): S(glast) covered PV(glast - 2), the one before it on this barrier, so the
       // parity is unambiguous (a parity wait tells apart two successive phases only)
-      ok = __all_sync(0xffffffffu, pipe_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
       if (!ok) break;
       if (active) {
         tc_fence_after();
