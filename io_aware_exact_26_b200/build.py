@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -51,6 +52,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def build_checks(force: bool = False) -> str:
     return _build_one(OUT_CHECKS, ["-DATTN_CHECKS"], force, False)
+
+
+def build_all() -> None:
+    """Both libraries, compiled side by side (each is one translation unit)."""
+    with ThreadPoolExecutor(2) as pool:
+        for job in (pool.submit(build), pool.submit(build_checks)):
+            job.result()
 
 
 if __name__ == "__main__":

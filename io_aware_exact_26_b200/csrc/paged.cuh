@@ -17,7 +17,6 @@
 // the workspace (two slots per CTA, independent of lengths) and the merge kernel joins
 // them in key order, so results do not depend on timing.
 #pragma once
-#include "bwd.cuh"     // bulk_load
 #include "cache.cuh"
 #include "fwd.cuh"
 
@@ -339,7 +338,7 @@ __device__ __forceinline__ void paged_pipe_init(PagedPipe& sh, int ring_consumer
     mbar_init(&sh.q8_full[i], C::K8 ? C::kWiden : 1);
   }
   for (int i = 0; i < C::KSK; ++i) {
-    mbar_init(&sh.k_full[i], C::KV8 && !C::K8 ? C::kWiden : 1);
+    mbar_init(&sh.k_full[i], C::K8 ? 33 : C::KV8 ? C::kWiden : 1);     // 33: the copies, and each lane's scales
     mbar_init(&sh.k_empty[i], 1);
   }
   for (int i = 0; i < C::KSV; ++i) {
@@ -347,7 +346,7 @@ __device__ __forceinline__ void paged_pipe_init(PagedPipe& sh, int ring_consumer
     mbar_init(&sh.v_empty[i], 1);
   }
   for (int i = 0; i < C::RST; ++i) {
-    mbar_init(&sh.raw_full[i], 1);
+    mbar_init(&sh.raw_full[i], 33);
     mbar_init(&sh.raw_empty[i], C::kWiden);
   }
   seg_ring_init(sh.ring, ring_consumers);
@@ -378,23 +377,45 @@ __device__ __forceinline__ PageTile page_tile(const PagedParams& p, const PagedS
   return t;
 }
 
-// Page of local box x of tile j, or -1 (recorded) if the table does not lead into the pool.
-__device__ __forceinline__ int page_of(const PagedParams& p, const PagedSeg& w, int j, int x) {
-  const int sh = p.c.page_shift;
-  const int pi = sh <= 7 ? (j << (7 - sh)) + x : j >> (sh - 7);
-  int page = -1;
-  if (pi < p.max_pages) page = p.table[static_cast<long long>(w.b) * p.max_pages + pi];
-  if (page < 0 || page >= p.c.num_pages) {
-    record_bad_page();
-    page = -1;
+// 128 successive entries of a sequence's row of the block table, 4 to a lane: the pages of
+// the next 16 or more key tiles.  Looking entries up one by one cost the producer a trip to
+// memory per tile (B = 64 requests of 8K, d = 64 bf16: 180 us; from here 143).
+struct PageWindow {
+  int e[4];
+  int base;                   // page index of the first one
+  __device__ __forceinline__ void load(const PagedParams& p, int b, int first, int lane) {
+    base = first;
+    const int* row = p.table + static_cast<long long>(b) * p.max_pages;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = first + 32 * i + lane < p.max_pages ? row[first + 32 * i + lane] : -1;
   }
-  return page;
+  // entry of page index pi (whole warp; any lane asks for its own, all within the window)
+  __device__ __forceinline__ int get(int pi) const {
+    const int off = pi - base;
+    int v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = __shfl_sync(0xffffffffu, e[i], off & 31);
+      if ((off >> 5) == i) v = x;
+    }
+    return v;
+  }
+};
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+// Arrive on the barrier once this thread's cp.async so far have landed (one of its count).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Producer warp: walks through the CTA's share, posts its pieces and brings in Q, K and V
 // (K and V tiles alternating).  Lane 0 arms a stage's barrier, then lane i issues the copy
-// of the tile's i-th (page, 64-column box), so small pages cost no more issue time than
-// large ones; the table entries of the next tile are read while this one is on its way.
+// of the tile's i-th (page, 64-column box).  A copy takes the copy engine some 60 ns however
+// small it is, so the scale bytes of an e4m3 tile, 16 to a page, do not go by copies of
+// their own: every lane fetches four of them by cp.async, which arrives on the same barrier.
 template <class C>
 __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tmq,
                                               const CUtensorMap* tmk, const CUtensorMap* tmv, const PagedSmem& m,
@@ -406,7 +427,7 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
   __syncwarp();
   PagedWalk walk;
   walk.begin(p, sh.plan, lane);
-  const int psh = p.c.page_shift < 7 ? p.c.page_shift : 7;
+  const int shift = p.c.page_shift, psh = shift < 7 ? shift : 7;
   const int rows = 1 << psh;                        // rows of a box
   constexpr int NX = C::KV8 ? 1 : C::NB;            // column boxes per page
   const int bx = lane / NX, bc = lane % NX;
@@ -414,12 +435,9 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const PagedSeg w = walk.next(p, sh.plan, cta);
-    int page = 0;
-    PageTile t{0, 0};
-    if (w.n > 0) {
-      t = page_tile(p, w, w.j0);
-      if (bx < t.count) page = page_of(p, w, w.j0, t.first + bx);
-    }
+    auto page_index = [&](int jt) { return shift <= 7 ? jt << (7 - shift) : jt >> (shift - 7); };   // tile's first page
+    PageWindow win;
+    if (w.n > 0) win.load(p, w.b, page_index(w.j0), lane);
     if (lane == 0) {
       ok = seg_ring_post(sh.ring, k, w);
       if (ok && w.n > 0) {
@@ -437,14 +455,24 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
     if (!ok || w.n == 0) break;
     for (int j = 0; j < w.n && ok; ++j, ++kc) {
       const int jt = w.j0 + j;
-      PageTile tn{0, 0};
-      int page_n = 0;
-      if (j + 1 < w.n) {
-        tn = page_tile(p, w, jt + 1);
-        if (bx < tn.count) page_n = page_of(p, w, jt + 1, tn.first + bx);     // in flight during this tile
+      const PageTile t = page_tile(p, w, jt);
+      const int p0 = page_index(jt);
+      if (p0 + (128 >> psh) > win.base + 128) win.load(p, w.b, p0, lane);
+      int page = win.get(p0 + min(t.first + bx, (128 >> psh) - 1));
+      if (bx < t.count && (page < 0 || page >= p.c.num_pages)) {
+        record_bad_page();
+        page = -1;
       }
-      const int y = p.c.page_shift > 7 ? (jt & ((1 << (p.c.page_shift - 7)) - 1)) * 128 : 0;
+      const int y = shift > 7 ? (jt & ((1 << (shift - 7)) - 1)) * 128 : 0;    // row of the tile in its page
       const int z = page < 0 ? p.c.num_pages : page;                          // outside the pool: zeros
+      // scale bytes of rows 4 lane .. 4 lane + 3; lane i holds the page of box i
+      long long scale_at = -1;
+      if constexpr (C::KV8) {
+        const int r = 4 * lane, box = (r >> psh) - t.first;
+        const int pg = __shfl_sync(0xffffffffu, page, box & 31);
+        if (box >= 0 && box < t.count && pg >= 0)
+          scale_at = ((static_cast<long long>(pg) * p.Hkv + w.g) << shift) + y + (r & (rows - 1));
+      }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         uint64_t *full, *empty;
@@ -475,32 +503,28 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
           empty = &sh.v_empty[st];
           dst = m.v + st * C::kTile;
         }
-        if (lane == 0) {
-          if (round > 0) ok = mbar_wait(empty, (round - 1) & 1);
-          if (ok) {
-            if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * (row_bytes + (C::KV8 ? 1 : 0)));
-            else mbar_arrive(full);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty, (round - 1) & 1));
         if (!ok) break;
+        if (lane == 0) {
+          if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * row_bytes);
+          else mbar_arrive(full);
+        }
+        __syncwarp();
         if (bx < t.count) {
           const int r0 = (t.first + bx) << psh;     // row of the box in the tile
           in_range(r0 + rows - 1, 128);
-          if constexpr (C::KV8) {
-            tma_load_4d(dst + r0 * row_bytes, kv ? tmv : tmk, full, 0, y, w.g, z);
-            const long long pg = page < 0 ? 0 : page;          // scale bytes of some page of the pool
-            bulk_load(scale + r0, (kv ? p.c.vs : p.c.ks) + (((pg * p.Hkv + w.g) << p.c.page_shift) + y), rows, full);
-          } else {
-            tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? tmv : tmk, full, bc * 64, y, w.g, z);
-          }
+          if constexpr (C::KV8) tma_load_4d(dst + r0 * row_bytes, kv ? tmv : tmk, full, 0, y, w.g, z);
+          else tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? tmv : tmk, full, bc * 64, y, w.g, z);
+        }
+        if constexpr (C::KV8) {
+          if (scale_at >= 0) cp_async4(scale + 4 * lane, (kv ? p.c.vs : p.c.ks) + scale_at);
+          cp_async_arrive(full);
         }
         nk = 2 * kc + kv + 1;
       }
-      page = page_n;
-      t = tn;
     }
   }
+  if constexpr (C::KV8) asm volatile("cp.async.wait_all;" ::: "memory");
   if (!ok && lane == 0) {                           // let copies in flight land
     for (int r = max(0, nk - 16); r < nk; ++r) {    // at most 8 stages of each kind: older ones have landed
       const int kt = r >> 1, kv = r & 1;

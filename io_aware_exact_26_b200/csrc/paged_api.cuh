@@ -154,11 +154,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int sme
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Query rows per item, by the batch's mean: 16 or 32 of the kernel for few rows where a
-// sequence's rows fit, else 128.  Any form is right for any lengths.
+// Query rows per item, by the batch's mean: the smallest build of the kernel for few rows
+// that takes a sequence's rows, else 128.  Any form is right for any lengths.
 int paged_form(int T, int B, int G) {
   const long long rows = static_cast<long long>(G) * ((T + B - 1) / B);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 
 // Workspace of the cut items: descriptors, LSE of the parts, then their O (fp32).
@@ -210,10 +210,14 @@ int launch_paged(Kernel kernel, const void* q, const attn_strides_t* q_strides, 
 template <int D, bool KV8>
 int launch_paged_form(int form, const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache,
                       const attn::PagedParams& p, cudaStream_t s) {
-  if (form == 16)
-    return launch_paged<attn::FewCfg<D, KV8, 16>>(attn::attn_paged_few_kernel<D, KV8, 16>, q, q_strides, cache, p, s);
-  if (form == 32)
-    return launch_paged<attn::FewCfg<D, KV8, 32>>(attn::attn_paged_few_kernel<D, KV8, 32>, q, q_strides, cache, p, s);
+#define ATTN_FEW(NR) \
+  if (form == NR) \
+    return launch_paged<attn::FewCfg<D, KV8, NR>>(attn::attn_paged_few_kernel<D, KV8, NR>, q, q_strides, cache, p, s);
+  ATTN_FEW(4)
+  ATTN_FEW(8)
+  ATTN_FEW(16)
+  ATTN_FEW(32)
+#undef ATTN_FEW
   return launch_paged<attn::RowsCfg<D, KV8>>(attn::attn_paged_rows_kernel<D, KV8>, q, q_strides, cache, p, s);
 }
 

@@ -4,10 +4,12 @@
 // A 128-row query tile would leave most softmax lanes idle here, and its two warps with
 // rows would take 1.3 us per key tile, more than a tile's bytes need from HBM at d = 64
 // (0.75 us) or with 8-bit keys.  So the products are turned around: keys fill the 128 rows
-// of the tensor-core tile and the NQ (16 or 32) query rows its columns,
+// of the tensor-core tile and the query rows its NQ columns,
 //     S^T = K Q^T   [128 keys x NQ],      O^T += V^T P^T   [d x NQ],
-// and a softmax thread owns a key, with NQ scores of its own: a tile takes 128 threads x
-// the rows there really are.  What crosses lanes is the maximum over keys, and softmax
+// and a softmax thread owns a key, with the scores of NR rows: the kernel is built for NR = 4,
+// 8, 16 and 32 rows per item (NQ = 16 is the least the tensor cores take), because a thread's
+// registers and the code's size follow NR (16 rows' code for 4 rows spent most of its time
+// on instruction fetches).  What crosses lanes is the maximum over keys, and softmax
 // needs no exact one: the exponent base of a row may be any number as long as O and the
 // sum use the same.  A tile's threads vote whether any score passes its row's base by
 // 2^kRescaleTau; only then (the first tiles of an item) are the maxima reduced, the base
@@ -38,9 +40,10 @@
 
 namespace attn {
 
-template <int D_, bool KV8_, int NQ>
+template <int D_, bool KV8_, int NR_>
 struct FewCfg {
-  static constexpr int D = D_;
+  static constexpr int D = D_, NR = NR_;
+  static constexpr int NQ = NR < 16 ? 16 : NR;     // columns of S^T and O^T
   static constexpr bool KV8 = KV8_, K8 = KV8_;
   static constexpr int kTile = 128 * D * 2;        // bf16 tile
   static constexpr int kBox = 128 * 128;
@@ -84,12 +87,12 @@ struct FewCfg {
   static_assert(!KV8 || RST >= 3, "too few raw stages");
 };
 
-template <int NQ>
+template <int NR>
 struct FewShared : PagedPipe {
-  float wmax[2][4][NQ];                // [group][warp]
-  float wsum[2][2][4][NQ];             // [piece parity][group][warp]
-  float base[2][2][NQ];                // [piece parity][group] exponent bases
-  float cq[4][NQ];                     // K8: 2^e of the query rows, by piece % 4
+  float wmax[2][4][NR];                // [group][warp]
+  float wsum[2][2][4][NR];             // [piece parity][group][warp]
+  float base[2][2][NR];                // [piece parity][group] exponent bases
+  alignas(16) float cq[4][NR];                    // K8: 2^e of the query rows, by piece % 4
   int vote[2][2][4];                   // [group][parity of its steps][warp]
   // By step % 4: S runs up to 3 steps ahead of P V, so a group may finish two of its steps
   // before the MMA warp looks at the first (a parity wait tells two successive phases apart).
@@ -100,15 +103,19 @@ struct FewShared : PagedPipe {
   uint64_t o_free;
 };
 
-// Reduction over the 32 lanes of NQ values per lane: each halving step exchanges half of
-// the values still held, so it takes NQ - 1 (+ 1) shuffles instead of 5 NQ.  Afterwards
-// v[0] holds the result of value few_owner(lane).
-template <int NQ, typename Op>
-__device__ __forceinline__ float few_reduce(float (&v)[NQ], int lane, Op op) {
+// Exponent base of a row that has seen no key: below every score, and 2^(it - score) is 0.
+constexpr float kNoBase = -3.0e38f;
+
+// Reduction over the 32 lanes of NR values per lane: each halving step exchanges half of
+// the values still held, so it takes fewer than NR + 5 shuffles instead of 5 NR.
+// Afterwards the returned value is that of row few_owner(lane).
+template <int NR, typename Op>
+__device__ __forceinline__ float few_reduce(float (&v)[NR], Op op) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int s = 0; s < 5; ++s) {
     const int off = 16 >> s;
-    const int half = NQ >> (s + 1);
+    const int half = NR >> (s + 1);
     if (half >= 1) {
       const bool up = (lane & off) != 0;
 #pragma unroll
@@ -123,21 +130,45 @@ __device__ __forceinline__ float few_reduce(float (&v)[NQ], int lane, Op op) {
   }
   return v[0];
 }
-template <int NQ>
-__device__ __forceinline__ int few_owner(int lane) {       // NQ = 32: the lane's bits; 16: without the last
-  return NQ == 32 ? lane : lane >> 1;
+template <int NR>
+__device__ __forceinline__ int few_owner(int lane) {       // the lane's upper log2(NR) bits
+  return lane / (32 / NR);
 }
 
-template <int NQ>
-__device__ __forceinline__ void few_tmem_ld(uint32_t addr, float (&f)[NQ]) {
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// NR columns of this thread's TMEM lane.
+template <int NR>
+__device__ __forceinline__ void few_tmem_ld(uint32_t addr, float (&f)[NR]) {
+  uint32_t r[NR];
+  if constexpr (NR == 4) tmem_ld4(addr, r);
+  else if constexpr (NR == 8) tmem_ld8(addr, r);
+  else if constexpr (NR == 16) tmem_ld16(addr, r);
+  else tmem_ld32(addr, r);
+  tmem_wait_ld();
+  reg_fence(r);
 #pragma unroll
-  for (int b = 0; b < NQ / 16; ++b) {
-    uint32_t r[16];
-    tmem_ld16(addr + b * 16, r);
-    tmem_wait_ld();
-    reg_fence(r);
+  for (int i = 0; i < NR; ++i) f[i] = __uint_as_float(r[i]);
+}
+template <int NR>
+__device__ __forceinline__ void few_tmem_st(uint32_t addr, const float (&f)[NR]) {
+  constexpr int N = NR < 16 ? NR : 16;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[b * 16 + i] = __uint_as_float(r[i]);
+  for (int b = 0; b < NR; b += N) {
+    uint32_t r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[b + i]);
+    if constexpr (N == 4) tmem_st4(addr + b, r);
+    else if constexpr (N == 8) tmem_st8(addr + b, r);
+    else tmem_st16(addr + b, r);
   }
 }
 
@@ -145,10 +176,10 @@ __device__ __forceinline__ void few_tmem_ld(uint32_t addr, float (&f)[NQ]) {
 __device__ __forceinline__ float e8m0_value(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
 
 // Q of a piece as hi + lo parts (see the head of this file), row scales to cq.
-template <class C, int NQ>
+template <class C>
 __device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float* cq, int wt) {
   constexpr int CPR = C::D / 8;                      // 8-value chunks per row, one per lane
-  for (int x = wt; x < NQ * CPR; x += 32 * C::kWiden) {
+  for (int x = wt; x < C::NR * CPR; x += 32 * C::kWiden) {
     const int r = x / CPR, c = x % CPR;
     const uint4 raw = *reinterpret_cast<const uint4*>(q + (c >> 3) * C::kQBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     float f[8];
@@ -187,15 +218,16 @@ __device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float
   }
 }
 
-template <int D, bool KV8, int NQ>
-__global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
+template <int D, bool KV8, int NR>
+__global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
     attn_paged_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const PagedParams p) {
-  using C = FewCfg<D, KV8, NQ>;
-  static_assert(sizeof(FewShared<NQ>) <= C::kShared, "FewShared does not fit its slot");
+  using C = FewCfg<D, KV8, NR>;
+  constexpr int NQ = C::NQ;
+  static_assert(sizeof(FewShared<NR>) <= C::kShared, "FewShared does not fit its slot");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  FewShared<NQ>& sh = *reinterpret_cast<FewShared<NQ>*>(smem + C::kOffSh);
+  FewShared<NR>& sh = *reinterpret_cast<FewShared<NR>*>(smem + C::kOffSh);
   const PagedSmem m = {smem + C::kOffQ,   smem + C::kOffK,     smem + C::kOffV,
                        smem + C::kOffRaw, smem + C::kOffScale, smem + C::kOffKScale};
   uint8_t* sQ8 = smem + C::kOffQ8;
@@ -316,7 +348,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
     if constexpr (KV8) {
       const int wt = threadIdx.x - 320;
       paged_widen<C>(sh, m, wt, lane, [&](int k, int qs) {
-        few_split_q<C, NQ>(m.q + qs * C::kQTile, sQ8 + qs * C::kQ8, sh.cq[k & 3], wt);
+        few_split_q<C>(m.q + qs * C::kQTile, sQ8 + qs * C::kQ8, sh.cq[k & 3], wt);
       });
     }
   } else {
@@ -341,10 +373,10 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
       // keys [all_lo, all_hi] are visible to every row
       const int all_hi = p.causal ? min(w.len - 1, w.pos0) : w.len - 1;
       const int all_lo = p.wl >= 0 ? w.pos0 + w.ntok - 1 - p.wl : 0;
-      float mu[NQ], ls[NQ];
+      float mu[NR], ls[NR];                                     // exponent bases, sums
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        mu[q] = -INFINITY;
+      for (int q = 0; q < NR; ++q) {
+        mu[q] = q < nrows ? kNoBase : INFINITY;                 // rows that are not there never vote
         ls[q] = 0.f;
       }
       const int g_end = gs + w.n;
@@ -353,32 +385,33 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g & 3], (g >> 2) & 1));
         if (!ok) break;
         tc_fence_after();
-        float x[NQ];
-        few_tmem_ld<NQ>(lane_base + (g & 3) * NQ, x);
+        float x[NR];
+        few_tmem_ld<NR>(lane_base + (g & 3) * NQ, x);
         float c = p.cs;
         if constexpr (KV8) {
           c *= e8m0_value(m.kscale[(g & 7) * 128 + row]);       // this key's scale
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) x[q] *= sh.cq[uq & 3][q];
+          for (int q = 0; q < NR; q += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sh.cq[uq & 3][q]);
+            x[q] *= f.x; x[q + 1] *= f.y; x[q + 2] *= f.z; x[q + 3] *= f.w;
+          }
         }
         const int k0 = (w.j0 + g - gs) * 128, key = k0 + row;
         bool up = false;
-        if (k0 >= all_lo && k0 + 127 <= all_hi) {
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            x[q] *= c;
-            up |= q < nrows && x[q] > mu[q] + kRescaleTau;
-          }
-        } else {
+        if (!(k0 >= all_lo && k0 + 127 <= all_hi)) {
           int i = 0, h = 0;                                     // token and head of row q
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
+          for (int q = 0; q < NR; ++q) {
             const int pos = w.pos0 + i;
             const bool see = key < w.len && (!p.causal || key <= pos) && (p.wl < 0 || key >= pos - p.wl);
-            x[q] = see ? x[q] * c : -INFINITY;
-            up |= q < nrows && x[q] > mu[q] + kRescaleTau;
+            if (!see) x[q] = -INFINITY;
             if (++h == p.G) { h = 0; ++i; }
           }
+        }
+#pragma unroll
+        for (int q = 0; q < NR; ++q) {
+          x[q] *= c;
+          up |= x[q] > mu[q] + kRescaleTau;
         }
         up = __any_sync(0xffffffffu, up);
         if (lane == 0) sh.vote[x2][par][wq] = up;
@@ -387,55 +420,45 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
         const volatile int* votes = sh.vote[x2][par];
         if (votes[0] | votes[1] | votes[2] | votes[3]) {
           {
-            float t[NQ];
+            float t[NR];
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) t[q] = x[q];
-            sh.wmax[x2][wq][few_owner<NQ>(lane)] =
-                few_reduce<NQ>(t, lane, [](float a, float b) { return fmaxf(a, b); });
+            for (int q = 0; q < NR; ++q) t[q] = x[q];
+            sh.wmax[x2][wq][few_owner<NR>(lane)] = few_reduce<NR>(t, [](float a, float b) { return fmaxf(a, b); });
           }
           ok = group_sync(&sh.xbar[x2], fs & 1);
           if (!ok) break;
           ++fs;
-          const bool again = g - 2 >= gs && has_o;              // O holds the group's steps before this one
-          if (again) {
+          float alpha[NR];
+#pragma unroll
+          for (int q = 0; q < NR; ++q) {
+            const float (&wm)[4][NR] = sh.wmax[x2];
+            const float top = fmaxf(fmaxf(wm[0][q], wm[1][q]), fmaxf(wm[2][q], wm[3][q]));
+            alpha[q] = 1.f;
+            if (top > mu[q]) {
+              alpha[q] = ex2_approx(mu[q] - top);
+              mu[q] = top;
+              ls[q] *= alpha[q];
+            }
+          }
+          if (g - 2 >= gs && has_o) {                           // O holds the group's steps before this one
             ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g - 2) & 3], ((g - 2) >> 2) & 1));
             if (!ok) break;
             tc_fence_after();
-          }
+            float o[NR];
+            few_tmem_ld<NR>(lane_base + C::kO + x2 * NQ, o);
 #pragma unroll
-          for (int b = 0; b < NQ / 16; ++b) {
-            uint32_t o[16];
-            if (again) {
-              tmem_ld16(lane_base + C::kO + x2 * NQ + b * 16, o);
-              tmem_wait_ld();
-              reg_fence(o);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int q = b * 16 + i;
-              const float (&wm)[4][NQ] = sh.wmax[x2];
-              const float top = fmaxf(fmaxf(wm[0][q], wm[1][q]), fmaxf(wm[2][q], wm[3][q]));
-              float alpha = 1.f;
-              if (top > mu[q]) {
-                alpha = mu[q] == -INFINITY ? 0.f : ex2_approx(mu[q] - top);
-                mu[q] = top;
-                ls[q] *= alpha;
-              }
-              if (again) o[i] = alpha == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * alpha);
-            }
-            if (again) tmem_st16(lane_base + C::kO + x2 * NQ + b * 16, o);
+            for (int q = 0; q < NR; ++q) o[q] = alpha[q] == 0.f ? 0.f : o[q] * alpha[q];
+            few_tmem_st<NR>(lane_base + C::kO + x2 * NQ, o);
+            tmem_wait_st();
           }
-          if (again) tmem_wait_st();
         }
         // P(g) takes the buffer of P(g - NP): PV(g - NP) is done, S(g) came behind it
         uint8_t* dst = prow + (g % C::NP) * C::kPTile;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (q < nrows) {
-            const float e = ex2_approx(x[q] - (mu[q] == -INFINITY ? 0.f : mu[q]));
-            ls[q] += e;
-            *reinterpret_cast<__nv_bfloat16*>(dst + q * 128 + (chunk ^ ((q & 7) << 4))) = __float2bfloat16_rn(e);
-          }
+        for (int q = 0; q < NR; ++q) {
+          const float e = ex2_approx(x[q] - mu[q]);
+          ls[q] += e;
+          *reinterpret_cast<__nv_bfloat16*>(dst + q * 128 + (chunk ^ ((q & 7) << 4))) = __float2bfloat16_rn(e);
         }
         tc_fence_before();
         fence_proxy_async_smem();
@@ -451,15 +474,11 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.o_free, (uq - 1) & 1));
         if (!ok) break;
       }
-      {
-        float t[NQ];
+      if (wq == 0 && lane == 0) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          t[q] = ls[q];
-          if (wq == 0 && lane == 0) sh.base[pp][x2][q] = mu[q];
-        }
-        sh.wsum[pp][x2][wq][few_owner<NQ>(lane)] = few_reduce<NQ>(t, lane, [](float a, float b) { return a + b; });
+        for (int q = 0; q < NR; ++q) sh.base[pp][x2][q] = mu[q];
       }
+      sh.wsum[pp][x2][wq][few_owner<NR>(lane)] = few_reduce<NR>(ls, [](float a, float b) { return a + b; });
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.done[pp]);
       gs = g_end;
@@ -470,39 +489,40 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NQ>::kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 3], (glast >> 2) & 1));
       if (!ok) break;
       tc_fence_after();
-      float o0[NQ], o1[NQ];
+      float o0[NR], o1[NR];
       if (has_o) {
-        few_tmem_ld<NQ>(lane_base + C::kO, o0);
-        few_tmem_ld<NQ>(lane_base + C::kO + NQ, o1);
+        few_tmem_ld<NR>(lane_base + C::kO, o0);
+        few_tmem_ld<NR>(lane_base + C::kO + NQ, o1);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_free);
       int i = 0, h = 0;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (q < nrows) {
-          const float m0 = sh.base[pp][0][q], m1 = sh.base[pp][1][q], top = fmaxf(m0, m1);
-          const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - top), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - top);
-          const float (&s0)[4][NQ] = sh.wsum[pp][0], (&s1)[4][NQ] = sh.wsum[pp][1];
-          const float l = ((s0[0][q] + s0[1][q]) + (s0[2][q] + s0[3][q])) * f0 +
-                          ((s1[0][q] + s1[1][q]) + (s1[2][q] + s1[3][q])) * f1;
-          const bool none = l == 0.f;                           // no key seen
-          const float val = none ? 0.f : ((f0 == 0.f ? 0.f : o0[q] * f0) + (f1 == 0.f ? 0.f : o1[q] * f1)) * (1.f / l);
-          const size_t orow = static_cast<size_t>(w.tok0 + i) * p.Hq + w.g * p.G + h;
-          const bool store = in_range(w.tok0 + i, p.T) && in_range(q, w.slot < 0 ? NQ : p.slot_rows);
-          const size_t part = static_cast<size_t>(w.slot < 0 ? 0 : w.slot) * p.slot_rows + q;
-          if (store && has_o) {
-            if (w.slot < 0) p.o[orow * D + row] = __float2bfloat16_rn(val);
-            else p.opart[part * D + row] = val;
-          }
-          if (store && row == q) {
-            const float lse = none ? -INFINITY : (top + __log2f(l)) * 0.69314718055994531f;
-            if (w.slot < 0) p.lse[orow] = lse;
-            else p.lpart[part] = lse;
-          }
-          if (++h == p.G) { h = 0; ++i; }
+      for (int q = 0; q < NR; ++q) {
+        if (q >= nrows) break;
+        const float m0 = sh.base[pp][0][q], m1 = sh.base[pp][1][q], top = fmaxf(m0, m1);
+        const float f0 = ex2_approx(m0 - top), f1 = ex2_approx(m1 - top);
+        const float (&s0)[4][NR] = sh.wsum[pp][0], (&s1)[4][NR] = sh.wsum[pp][1];
+        const float l0 = (s0[0][q] + s0[1][q]) + (s0[2][q] + s0[3][q]);
+        const float l1 = (s1[0][q] + s1[1][q]) + (s1[2][q] + s1[3][q]);
+        const float l = l0 * f0 + l1 * f1;
+        const bool none = l == 0.f;                             // no key seen
+        // a group that saw nothing has l = 0, and anything in its columns of O
+        const float val = none ? 0.f : ((l0 == 0.f ? 0.f : o0[q] * f0) + (l1 == 0.f ? 0.f : o1[q] * f1)) * (1.f / l);
+        const size_t orow = static_cast<size_t>(w.tok0 + i) * p.Hq + w.g * p.G + h;
+        const bool store = in_range(w.tok0 + i, p.T) && in_range(q, w.slot < 0 ? NR : p.slot_rows);
+        const size_t part = static_cast<size_t>(w.slot < 0 ? 0 : w.slot) * p.slot_rows + q;
+        if (store && has_o) {
+          if (w.slot < 0) p.o[orow * D + row] = __float2bfloat16_rn(val);
+          else p.opart[part * D + row] = val;
         }
+        if (store && row == q) {
+          const float lse = none ? -INFINITY : (top + __log2f(l)) * 0.69314718055994531f;
+          if (w.slot < 0) p.lse[orow] = lse;
+          else p.lpart[part] = lse;
+        }
+        if (++h == p.G) { h = 0; ++i; }
       }
       ++uq;
     }
