@@ -321,7 +321,8 @@ __device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddep
 // Barriers between the producer warp, the widening warps (e4m3 cache) and the MMA warp.
 struct PagedPipe {
   uint64_t q_full[2], q_empty[2], q8_full[2];
-  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t k_full[8], v_full[8];       // by stage: the tile is there
+  uint64_t k_done[8], v_done[8];       // by tile % 8: S, and P V, of that tile complete
   uint64_t raw_full[8], raw_empty[8];
   SegRing ring;
   uint64_t drain, teardown;
@@ -338,20 +339,28 @@ __device__ __forceinline__ void paged_pipe_init(PagedPipe& sh, int ring_consumer
     mbar_init(&sh.q8_full[i], C::K8 ? C::kWiden : 1);
   }
   for (int i = 0; i < C::KSK; ++i) {
-    mbar_init(&sh.k_full[i], C::K8 ? 33 : C::KV8 ? C::kWiden : 1);     // 33: the copies, and each lane's scales
-    mbar_init(&sh.k_empty[i], 1);
+    mbar_init(&sh.k_full[i], C::K8 ? 33 : C::KV8 ? 4 : 1);     // 33: the copies, and each lane's scales
   }
   for (int i = 0; i < C::KSV; ++i) {
-    mbar_init(&sh.v_full[i], C::KV8 ? C::kWiden : 1);
-    mbar_init(&sh.v_empty[i], 1);
+    mbar_init(&sh.v_full[i], C::KV8 ? 4 : 1);
+  }
+  for (int i = 0; i < 8; ++i) {
+    mbar_init(&sh.k_done[i], 1);
+    mbar_init(&sh.v_done[i], 1);
   }
   for (int i = 0; i < C::RST; ++i) {
     mbar_init(&sh.raw_full[i], 33);
-    mbar_init(&sh.raw_empty[i], C::kWiden);
+    mbar_init(&sh.raw_empty[i], 4);
   }
   seg_ring_init(sh.ring, ring_consumers);
   mbar_init(&sh.drain, 1);
   mbar_init(&sh.teardown, warps);
+}
+
+// Wait until S (P V) of tile c, counted over the CTA's share, is complete: its K (V) stage
+// may be filled again.
+__device__ __forceinline__ bool tile_done_wait(uint64_t (&done)[8], int c) {
+  return mbar_wait(&done[c & 7], (c >> 3) & 1);
 }
 
 // Shared-memory regions of a kernel.
@@ -411,33 +420,102 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Producer warp: walks through the CTA's share, posts its pieces and brings in Q, K and V
-// (K and V tiles alternating).  Lane 0 arms a stage's barrier, then lane i issues the copy
-// of the tile's i-th (page, 64-column box).  A copy takes the copy engine some 60 ns however
-// small it is, so the scale bytes of an e4m3 tile, 16 to a page, do not go by copies of
-// their own: every lane fetches four of them by cp.async, which arrives on the same barrier.
+// Copies of one tensor's key tiles of a piece: kv = 0 K, 1 V; kc counts the tiles before it.
+// Lane 0 arms a stage's barrier, then lane i issues the copy of the tile's i-th (page,
+// 64-column box).  A copy takes the copy engine some 60 ns however small it is, so the scale
+// bytes of an e4m3 tile, 16 to a page, do not go by copies of their own: every lane fetches
+// four of them by cp.async, which arrives on the same barrier.
+template <class C, int kv>
+__device__ __forceinline__ bool paged_load_tiles(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tm,
+                                                 const PagedSmem& m, const PagedSeg& w, int& kc, int lane) {
+  constexpr bool kRaw = C::KV8 && !(C::K8 && kv == 0);         // e4m3 tiles on their way to be widened
+  // bytes per key that the copies bring in: a padded e4m3 row of 128 bytes for K8
+  constexpr int kRowBytes = kv == 0 && C::K8 ? 128 : C::KV8 ? C::D : 2 * C::D;
+  constexpr int kStages = kRaw ? C::kRawMod : kv == 0 ? C::KSK : C::KSV;
+  constexpr int NX = C::KV8 ? 1 : C::NB;                       // column boxes per page
+  const int shift = p.c.page_shift, psh = shift < 7 ? shift : 7;
+  const int rows = 1 << psh, per_tile = 128 >> psh;            // rows of a box, pages of a tile
+  const int bx = lane / NX, bc = lane % NX;
+  PageWindow win;
+  int p0 = shift <= 7 ? w.j0 << (7 - shift) : w.j0 >> (shift - 7);
+  win.load(p, w.b, p0, lane);
+  for (int j = 0; j < w.n; ++j, ++kc) {
+    const int jt = w.j0 + j;
+    const PageTile t = page_tile(p, w, jt);
+    p0 = shift <= 7 ? jt << (7 - shift) : jt >> (shift - 7);
+    if (p0 + per_tile > win.base + 128) win.load(p, w.b, p0, lane);
+    int page = win.get(p0 + min(t.first + bx, per_tile - 1));
+    if (bx < t.count && (page < 0 || page >= p.c.num_pages)) {
+      record_bad_page();
+      page = -1;
+    }
+    const int y = shift > 7 ? (jt & ((1 << (shift - 7)) - 1)) * 128 : 0;      // row of the tile in its page
+    // a stage and which use of it this is (K8 = false: K and V share the raw stages in turn)
+    const int c = kRaw && !C::K8 ? 2 * kc + kv : kc;
+    const int st = c % kStages, round = c / kStages;
+    uint64_t* full = kRaw ? &sh.raw_full[st] : kv == 0 ? &sh.k_full[st] : &sh.v_full[st];
+    uint8_t* dst = kRaw ? m.raw + st * C::kRawTile : kv == 0 ? m.k + st * C::kKTile : m.v + st * C::kTile;
+    const uint8_t* scale_src = nullptr;             // scale bytes of rows 4 lane .. 4 lane + 3
+    if constexpr (C::KV8) {
+      const int r = 4 * lane, box = (r >> psh) - t.first;
+      const int pg = __shfl_sync(0xffffffffu, page, box & 31);                // lane i holds the page of box i
+      if (box >= 0 && box < t.count && pg >= 0)
+        scale_src = (kv ? p.c.vs : p.c.ks) + (((static_cast<long long>(pg) * p.Hkv + w.g) << shift) + y + (r & (rows - 1)));
+    }
+    if (round > 0) {
+      const bool free = kRaw ? mbar_wait(&sh.raw_empty[st], (round - 1) & 1)
+                             : tile_done_wait(kv ? sh.v_done : sh.k_done, kc - kStages);
+      if (!__all_sync(0xffffffffu, free)) return false;
+    }
+    if (lane == 0) {
+      if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * kRowBytes);
+      else mbar_arrive(full);
+    }
+    __syncwarp();
+    if (bx < t.count) {
+      const int r0 = (t.first + bx) << psh;         // row of the box in the tile
+      in_range(r0 + rows - 1, 128);
+      const int z = page < 0 ? p.c.num_pages : page;           // outside the pool: zeros
+      tma_load_4d(dst + (C::KV8 ? r0 * kRowBytes : bc * C::kBox + r0 * 128), tm, full, C::KV8 ? 0 : bc * 64, y, w.g, z);
+    }
+    if constexpr (C::KV8) {
+      uint8_t* scale = kRaw ? m.scale + st * 128 : m.kscale + (kc & 7) * 128;
+      if (scale_src) cp_async4(scale + 4 * lane, scale_src);
+      cp_async_arrive(full);
+    }
+  }
+  return true;
+}
+
+// On an error: let the copies in flight of one tensor land (bounded); kc tiles were begun.
+template <class C, int kv>
+__device__ __forceinline__ void paged_drain_tiles(PagedPipe& sh, int kc, int lane) {
+  constexpr bool kRaw = C::KV8 && !(C::K8 && kv == 0);
+  constexpr int kStages = kRaw ? C::kRawMod : kv == 0 ? C::KSK : C::KSV;
+  if constexpr (C::KV8) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (lane != 0) return;
+  for (int t = max(0, kc - kStages); t <= kc; ++t) {
+    const int c = kRaw && !C::K8 ? 2 * t + kv : t;
+    uint64_t* full = kRaw ? &sh.raw_full[c % kStages] : kv == 0 ? &sh.k_full[c % kStages] : &sh.v_full[c % kStages];
+    mbar_drain_wait(full, (c / kStages) & 1);
+  }
+}
+
+// K producer warp: walks through the CTA's share, posts its pieces and brings in Q and K.
 template <class C>
-__device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tmq,
-                                              const CUtensorMap* tmk, const CUtensorMap* tmv, const PagedSmem& m,
-                                              int cta, int lane) {
+__device__ __forceinline__ void paged_produce_k(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tmq,
+                                                const CUtensorMap* tmk, const PagedSmem& m, int cta, int lane) {
   if (lane == 0) {
-    tma_prefetch_desc(tmq); tma_prefetch_desc(tmk); tma_prefetch_desc(tmv);
+    tma_prefetch_desc(tmq); tma_prefetch_desc(tmk);
     p.cuts[cta].ntok = 0;
   }
   __syncwarp();
   PagedWalk walk;
   walk.begin(p, sh.plan, lane);
-  const int shift = p.c.page_shift, psh = shift < 7 ? shift : 7;
-  const int rows = 1 << psh;                        // rows of a box
-  constexpr int NX = C::KV8 ? 1 : C::NB;            // column boxes per page
-  const int bx = lane / NX, bc = lane % NX;
-  int kc = 0, nk = 0, uq = 0;                       // key tiles, K/V stages armed, pieces
+  int kc = 0, uq = 0;                               // key tiles, pieces
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const PagedSeg w = walk.next(p, sh.plan, cta);
-    auto page_index = [&](int jt) { return shift <= 7 ? jt << (7 - shift) : jt >> (shift - 7); };   // tile's first page
-    PageWindow win;
-    if (w.n > 0) win.load(p, w.b, page_index(w.j0), lane);
     if (lane == 0) {
       ok = seg_ring_post(sh.ring, k, w);
       if (ok && w.n > 0) {
@@ -453,98 +531,39 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, PagedPipe& s
     }
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     if (!ok || w.n == 0) break;
-    for (int j = 0; j < w.n && ok; ++j, ++kc) {
-      const int jt = w.j0 + j;
-      const PageTile t = page_tile(p, w, jt);
-      const int p0 = page_index(jt);
-      if (p0 + (128 >> psh) > win.base + 128) win.load(p, w.b, p0, lane);
-      int page = win.get(p0 + min(t.first + bx, (128 >> psh) - 1));
-      if (bx < t.count && (page < 0 || page >= p.c.num_pages)) {
-        record_bad_page();
-        page = -1;
-      }
-      const int y = shift > 7 ? (jt & ((1 << (shift - 7)) - 1)) * 128 : 0;    // row of the tile in its page
-      const int z = page < 0 ? p.c.num_pages : page;                          // outside the pool: zeros
-      // scale bytes of rows 4 lane .. 4 lane + 3; lane i holds the page of box i
-      long long scale_at = -1;
-      if constexpr (C::KV8) {
-        const int r = 4 * lane, box = (r >> psh) - t.first;
-        const int pg = __shfl_sync(0xffffffffu, page, box & 31);
-        if (box >= 0 && box < t.count && pg >= 0)
-          scale_at = ((static_cast<long long>(pg) * p.Hkv + w.g) << shift) + y + (r & (rows - 1));
-      }
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint64_t *full, *empty;
-        uint8_t *dst, *scale = nullptr;
-        int st, round;                              // stage, and which use of it this is
-        // bytes per key that the copies bring in: a padded e4m3 row of 128 bytes for K8
-        constexpr int kRow8 = C::KV8 ? C::D : 2 * C::D;
-        const int row_bytes = kv == 0 && C::K8 ? 128 : kRow8;
-        if (C::KV8 && !(C::K8 && kv == 0)) {
-          const int rc = C::K8 ? kc : 2 * kc + kv;
-          st = rc % C::kRawMod;
-          round = rc / C::kRawMod;
-          full = &sh.raw_full[st];
-          empty = &sh.raw_empty[st];
-          dst = m.raw + st * C::kRawTile;
-          scale = m.scale + st * 128;
-        } else if (kv == 0) {
-          st = kc % C::KSK;
-          round = kc / C::KSK;
-          full = &sh.k_full[st];
-          empty = &sh.k_empty[st];
-          dst = m.k + st * C::kKTile;
-          scale = m.kscale + (kc & 7) * 128;
-        } else {
-          st = kc % C::KSV;
-          round = kc / C::KSV;
-          full = &sh.v_full[st];
-          empty = &sh.v_empty[st];
-          dst = m.v + st * C::kTile;
-        }
-        if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty, (round - 1) & 1));
-        if (!ok) break;
-        if (lane == 0) {
-          if (t.count > 0) mbar_arrive_expect_tx(full, t.count * rows * row_bytes);
-          else mbar_arrive(full);
-        }
-        __syncwarp();
-        if (bx < t.count) {
-          const int r0 = (t.first + bx) << psh;     // row of the box in the tile
-          in_range(r0 + rows - 1, 128);
-          if constexpr (C::KV8) tma_load_4d(dst + r0 * row_bytes, kv ? tmv : tmk, full, 0, y, w.g, z);
-          else tma_load_4d(dst + bc * C::kBox + r0 * 128, kv ? tmv : tmk, full, bc * 64, y, w.g, z);
-        }
-        if constexpr (C::KV8) {
-          if (scale_at >= 0) cp_async4(scale + 4 * lane, (kv ? p.c.vs : p.c.ks) + scale_at);
-          cp_async_arrive(full);
-        }
-        nk = 2 * kc + kv + 1;
-      }
-    }
+    ok = paged_load_tiles<C, 0>(p, sh, tmk, m, w, kc, lane);
+  }
+  if (!ok) {
+    paged_drain_tiles<C, 0>(sh, kc, lane);
+    if (lane == 0)
+      for (int r = max(0, uq - C::QST); r < uq; ++r) mbar_drain_wait(&sh.q_full[r % C::QST], (r / C::QST) & 1);
   }
   if constexpr (C::KV8) asm volatile("cp.async.wait_all;" ::: "memory");
-  if (!ok && lane == 0) {                           // let copies in flight land
-    for (int r = max(0, nk - 16); r < nk; ++r) {    // at most 8 stages of each kind: older ones have landed
-      const int kt = r >> 1, kv = r & 1;
-      if (C::KV8 && !(C::K8 && kv == 0)) {
-        const int rc = C::K8 ? kt : r;
-        if (rc >= (C::K8 ? (nk + 1) / 2 : nk) - C::RST)
-          mbar_drain_wait(&sh.raw_full[rc % C::kRawMod], (rc / C::kRawMod) & 1);
-      } else if (kv == 0) {
-        if (kt >= (nk + 1) / 2 - C::KSK) mbar_drain_wait(&sh.k_full[kt % C::KSK], (kt / C::KSK) & 1);
-      } else {
-        if (kt >= (nk + 1) / 2 - C::KSV) mbar_drain_wait(&sh.v_full[kt % C::KSV], (kt / C::KSV) & 1);
-      }
-    }
-    for (int r = max(0, uq - C::QST); r < uq; ++r) mbar_drain_wait(&sh.q_full[r % C::QST], (r / C::QST) & 1);
-  }
   __syncwarp();
 }
 
-// Widening warps (e4m3 cache), wt = 0 .. 32 kWiden - 1; split_q(k, qs) readies Q of the k-th
-// piece in buffer qs (K8).  A lane takes 16 codes of a row,
+// V producer warp: follows the posted pieces (one warp for both tensors took 1.9k cycles
+// per tile at work of its own, more than an e4m3 tile's 1.4k at HBM's rate).
+template <class C>
+__device__ __forceinline__ void paged_produce_v(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tmv,
+                                                const PagedSmem& m, int lane) {
+  if (lane == 0) tma_prefetch_desc(tmv);
+  int kc = 0;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
+    if (w.n == 0) break;
+    ok = paged_load_tiles<C, 1>(p, sh, tmv, m, w, kc, lane);
+  }
+  if (!ok) paged_drain_tiles<C, 1>(sh, kc, lane);
+  if constexpr (C::KV8) asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+}
+
+// Widening warps (e4m3 cache), wt = 0 .. 32 kWiden - 1, in groups of four: each group takes
+// whole tiles in turn (K8: the V tiles; else group 0 those of K, group 1 those of V), so
+// that a tile's waits and fences overlap the other group's work.  split_q(k, qs) readies Q
+// of the k-th piece in buffer qs (K8).  A lane takes 16 codes of a row,
 // widens them with the row's scale and stores two 16-byte chunks of the bf16 tile in the
 // 128B-swizzled layout the TMA would write.  Eight lanes (one shared-memory wavefront)
 // take 4 chunks of each of 2 rows: their stores then fall on 8 different chunk positions.
@@ -555,7 +574,10 @@ template <class C, typename SplitQ>
 __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, int wt, int lane, SplitQ split_q) {
   constexpr int D = C::D;
   constexpr int CPR = D / 16;                       // 16-code chunks per row
-  constexpr int RPP = 32 * C::kWiden / CPR;         // rows per pass
+  constexpr int RPP = 128 / CPR;                    // rows per pass of a group
+  constexpr int kGroups = C::kWiden / 4;
+  const int grp = wt >> 7;
+  wt &= 127;
   const int e = wt & 3, half = (wt >> 3) & 1;       // chunk inside its set, which set (d = 128)
   const int c = D == 128 ? (e ^ ((e & 1) << 2) ^ half) : e;
   const int r_in = D == 128 ? ((wt >> 4) << 1) + ((wt >> 2) & 1) : wt >> 2;
@@ -579,10 +601,11 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
       const int st = kc % C::KSV;
 #pragma unroll 1
       for (int kv = C::K8 ? 1 : 0; kv < 2; ++kv) {
+        if ((C::K8 ? kc : kv) % kGroups != grp) continue;
         const int rc = C::K8 ? kc : 2 * kc + kv, rs = rc % C::RST;
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.raw_full[rs], (rc / C::RST) & 1));
         if (ok && kc >= C::KSV)
-          ok = __all_sync(0xffffffffu, mbar_wait(kv ? &sh.v_empty[st] : &sh.k_empty[st], ((kc / C::KSV) - 1) & 1));
+          ok = __all_sync(0xffffffffu, tile_done_wait(kv ? sh.v_done : sh.k_done, kc - C::KSV));
         if (!ok) break;
         const uint8_t* raw = m.raw + rs * C::kRawTile;
         uint8_t* out = (kv ? m.v : m.k) + st * C::kTile;
@@ -605,29 +628,33 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
           *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
         };
-        uint32_t codes[NP][4];
-        int byte[NP];
-        bool rare = false;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          load(i, codes[i], byte[i]);
-          rare |= byte[i] > kE4m3FastByte || e4m3_any_nan<4>(codes[i]) != 0;
-        }
-        if (!__any_sync(0xffffffffu, rare)) {       // one branch for the warp and the tile
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            uint32_t y[8];
-            e4m3_widen<4>(codes[i], byte[i], false, y);
-            put(i, y);
-          }
-        } else {
+        constexpr int NB = NP < 4 ? NP : 4;         // passes whose loads are in flight together
 #pragma unroll 1
-          for (int i = 0; i < NP; ++i) {
-            uint32_t again[4], y[8];
-            int b;
-            load(i, again, b);
-            e4m3_widen<4>(again, b, true, y);
-            put(i, y);
+        for (int i0 = 0; i0 < NP; i0 += NB) {
+          uint32_t codes[NB][4];
+          int byte[NB];
+          bool rare = false;
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            load(i0 + i, codes[i], byte[i]);
+            rare |= byte[i] > kE4m3FastByte || e4m3_any_nan<4>(codes[i]) != 0;
+          }
+          if (!__any_sync(0xffffffffu, rare)) {     // one branch for the warp
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              uint32_t y[8];
+              e4m3_widen<4>(codes[i], byte[i], false, y);
+              put(i0 + i, y);
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < NB; ++i) {
+              uint32_t again[4], y[8];
+              int b;
+              load(i0 + i, again, b);
+              e4m3_widen<4>(again, b, true, y);
+              put(i0 + i, y);
+            }
           }
         }
         fence_proxy_async_smem();                   // generic-proxy writes -> tensor-core reads

@@ -21,9 +21,10 @@
 //
 //   warps 0-3, 4-7  softmax groups 0, 1: group g % 2 takes step g (thread = key of the tile =
 //                   TMEM lane); the epilogue is group 0's (thread = column of O)
-//   warp 8          producer (paged_produce)
-//   warp 9          MMA issuer: S runs SA steps ahead in 4 buffers of NQ columns
-//   warps 10-       widening warps (e4m3 cache)
+//   warps 8, 9      producers of K (and Q) and of V
+//   warp 10         MMA issuer: S runs SA steps ahead of P V, in 4 buffers of NQ columns.  (A
+//                   warp for each product measured 17% slower with an e4m3 cache.)
+//   warps 11-       widening warps (e4m3 cache)
 // P goes through shared memory (K-major, 128B swizzle) as the second operand of O^T; V is
 // read column-major as the first.  At d = 64 the 128 rows of O^T hold d in the first 64;
 // the others come from the 16 KB behind the V tile and are never read.
@@ -59,9 +60,11 @@ struct FewCfg {
   // S(g) completes behind PV(g - SA), so P(g) may take the buffer of P(g - NP) for NP >= SA
   static constexpr int SA = NQ == 16 ? 3 : 2;
   static constexpr int NP = NQ == 16 ? 4 : 2;
-  static_assert(SA <= KSK && SA <= KSV + 1 && NP >= SA && (!K8 || KSK + SA + 1 <= 8), "stages");
+  // K8: the scale bytes of the last 8 K tiles are kept: a tile is filled in KSK tiles ahead of
+  // S, S runs SA ahead of the softmax
+  static_assert(SA <= KSK && SA <= KSV + 1 && NP >= SA && KSK <= 8 && KSV <= 8 && (!K8 || KSK + SA + 1 <= 8), "stages");
   static constexpr int kWiden = KV8 ? (NQ == 16 ? 8 : 4) : 0;
-  static constexpr int kThreads = 320 + 32 * kWiden;
+  static constexpr int kThreads = 352 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;
   static constexpr int kShared = NQ == 16 ? 4096 : 6144;
   static constexpr int kRoom = 232448 - 1024 - KSK * kKTile - KSV * kTile - QST * (kQTile + kQ8) - NP * kPTile -
@@ -96,7 +99,7 @@ struct FewShared : PagedPipe {
   int vote[2][2][4];                   // [group][parity of its steps][warp]
   // By step % 4: S runs up to 3 steps ahead of P V, so a group may finish two of its steps
   // before the MMA warp looks at the first (a parity wait tells two successive phases apart).
-  uint64_t s_full[4], p_ready[4], pv_done[4];
+  uint64_t p_ready[4];
   uint64_t vbar[2][2];                 // [group][parity of its steps]: its four warps voted
   uint64_t xbar[2];                    // [group]: its four warps posted their maxima
   uint64_t done[2];                    // [piece parity]: all eight warps posted sums and bases
@@ -236,10 +239,8 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    paged_pipe_init<C>(sh, 9 + C::kWiden, 10 + C::kWiden);
+    paged_pipe_init<C>(sh, 10 + C::kWiden, 11 + C::kWiden);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.p_ready[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -261,9 +262,11 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == 8) {
-    paged_produce<C>(p, sh, &tmq, &tmk, &tmv, m, cta, lane);
+    paged_produce_k<C>(p, sh, &tmq, &tmk, m, cta, lane);
   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
+    paged_produce_v<C>(p, sh, &tmv, m, lane);
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ MMA issuer (one thread)
     const bool leader = elect_one();
     constexpr uint32_t idS = KV8 ? idesc_e4m3_f32(128, NQ, false, false) : idesc_bf16_f32(128, NQ, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(128, NQ, true, false);
@@ -272,81 +275,69 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
     const uint32_t k_lo0 = sdesc_lo(smem_u32(m.k), 16);
     const uint32_t v_lo0 = sdesc_lo(smem_u32(m.v), C::kBox);
     const uint32_t p_lo0 = sdesc_lo(smem_u32(sP), 16);
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-    };
-    int kc = 0, vc = 0, gs = 0, uq = 0;
+    int gs = 0;                                     // steps before the piece
     bool ok = true;
-    // S^T(g) = K(kc) Q^T into buffer g % 4.  Its last reader arrived on p_ready for step
-    // g - 4, which PV(g - 4), issued before, waited for.
-    auto issue_s = [&](int g, int qs, bool last) -> bool {
-      const int st = kc % C::KSK;
-      if (!wait(&sh.k_full[st], (kc / C::KSK) & 1)) return false;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t k_lo = k_lo0 + st * (C::kKTile >> 4);
-        const uint32_t d = tmem + (g & 3) * NQ;
-        if constexpr (KV8) {
-          const uint32_t q_lo = q_lo0 + qs * (C::kQ8 >> 4);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              umma_ss_f8_lo(d, k_lo + ((k * 32) >> 4), q_lo + ((part * C::kQBox + k * 32) >> 4), hi, idS,
-                            part + k > 0);
-        } else {
-          const uint32_t q_lo = q_lo0 + qs * (C::kQTile >> 4);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            umma_ss_lo(d, k_lo + (((k >> 2) * C::kBox + (k & 3) * 32) >> 4),
-                       q_lo + (((k >> 2) * C::kQBox + (k & 3) * 32) >> 4), hi, idS, k > 0);
-        }
-        umma_commit(&sh.s_full[g & 3]);
-        umma_commit(&sh.k_empty[st]);
-        if (last) umma_commit(&sh.q_empty[qs]);
-      }
-      __syncwarp();
-      ++kc;
-      return true;
-    };
     for (int k = 0; ok; ++k) {
       const PagedSeg w = seg_ring_take(sh.ring, k, lane, ok);
       if (w.n == 0) break;
-      const int qs = uq % C::QST;
-      ok = wait(KV8 ? &sh.q8_full[qs] : &sh.q_full[qs], (uq / C::QST) & 1);
-      for (int t = 0; t < C::SA && t < w.n && ok; ++t) ok = issue_s(gs + t, qs, t == w.n - 1);
-      for (int j = 0; j < w.n && ok; ++j, ++vc) {
-        const int g = gs + j, vst = vc % C::KSV;
-        ok = wait(&sh.v_full[vst], (vc / C::KSV) & 1);
-        if (!KV8 && ok) paged_zero_v<C>(w, j, m.v + vst * C::kTile, lane);
-        if (ok) ok = wait(&sh.p_ready[g & 3], (g >> 2) & 1);
-        if (ok && j == 0 && uq >= 1) ok = wait(&sh.o_free, (uq - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t v_lo = v_lo0 + vst * (C::kTile >> 4);
-          const uint32_t p_lo = p_lo0 + (g % C::NP) * (C::kPTile >> 4);
+      if (leader) {
+        const int qs = k % C::QST;
+        ok = mbar_wait(KV8 ? &sh.q8_full[qs] : &sh.q_full[qs], (k / C::QST) & 1);
+        const uint32_t q_lo = q_lo0 + qs * ((KV8 ? C::kQ8 : C::kQTile) >> 4);
+        // S^T(g) = K Q^T into buffer g % 4.  Its last reader arrived on p_ready for step g - 4,
+        // which PV(g - 4), issued before, waited for.
+        auto issue_s = [&](int g) {
+          const int st = g % C::KSK;
+          if (!mbar_wait(&sh.k_full[st], (g / C::KSK) & 1)) return false;
+          tc_fence_after();
+          const uint32_t k_lo = k_lo0 + st * (C::kKTile >> 4), d = tmem + (g & 3) * NQ;
+          if constexpr (KV8) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k2 = 0; k2 < D / 32; ++k2)
+                umma_ss_f8_lo(d, k_lo + ((k2 * 32) >> 4), q_lo + ((part * C::kQBox + k2 * 32) >> 4), hi, idS,
+                              part + k2 > 0);
+          } else {
+#pragma unroll
+            for (int k2 = 0; k2 < D / 16; ++k2)
+              umma_ss_lo(d, k_lo + (((k2 >> 2) * C::kBox + (k2 & 3) * 32) >> 4),
+                         q_lo + (((k2 >> 2) * C::kQBox + (k2 & 3) * 32) >> 4), hi, idS, k2 > 0);
+          }
+          umma_commit(&sh.k_done[g & 7]);
+          if (g == gs + w.n - 1) umma_commit(&sh.q_empty[qs]);
+          return true;
+        };
+        for (int t = 0; t < C::SA && t < w.n && ok; ++t) ok = issue_s(gs + t);
+        if (ok && k >= 1) ok = mbar_wait(&sh.o_free, (k - 1) & 1);
+        for (int j = 0; j < w.n && ok; ++j) {
+          // O^T of group g % 2 (+)= V^T P^T(g); the group's first step of a piece starts it
+          const int g = gs + j, st = g % C::KSV;
+          ok = mbar_wait(&sh.v_full[st], (g / C::KSV) & 1);
+          if (ok) ok = mbar_wait(&sh.p_ready[g & 3], (g >> 2) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_lo = v_lo0 + st * (C::kTile >> 4), p_lo = p_lo0 + (g % C::NP) * (C::kPTile >> 4);
+          const uint32_t d = tmem + C::kO + (g & 1) * NQ;
 #pragma unroll
           for (int k2 = 0; k2 < 8; ++k2)
-            umma_ss_lo(tmem + C::kO + (g & 1) * NQ, v_lo + ((k2 * 2048) >> 4),
-                       p_lo + (((k2 >> 2) * C::kQBox + (k2 & 3) * 32) >> 4), hi, idO, !(j < 2 && k2 == 0));
-          umma_commit(&sh.pv_done[g & 3]);
-          umma_commit(&sh.v_empty[vst]);
+            umma_ss_lo(d, v_lo + ((k2 * 2048) >> 4), p_lo + (((k2 >> 2) * C::kQBox + (k2 & 3) * 32) >> 4), hi, idO,
+                       !(j < 2 && k2 == 0));
+          umma_commit(&sh.v_done[g & 7]);
+          if (j + C::SA < w.n) ok = issue_s(g + C::SA);
         }
-        __syncwarp();
-        if (j + C::SA < w.n) ok = issue_s(g + C::SA, qs, j + C::SA == w.n - 1);
       }
+      ok = __all_sync(0xffffffffu, ok);
       gs += w.n;
-      ++uq;
     }
     if (leader) {
       umma_commit(&sh.drain);
       mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp >= 11) {
     if constexpr (KV8) {
-      const int wt = threadIdx.x - 320;
+      const int wt = threadIdx.x - 352;
       paged_widen<C>(sh, m, wt, lane, [&](int k, int qs) {
         few_split_q<C>(m.q + qs * C::kQTile, sQ8 + qs * C::kQ8, sh.cq[k & 3], wt);
       });
@@ -382,7 +373,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
       const int g_end = gs + w.n;
       for (int g = gs + ((gs ^ x2) & 1); g < g_end; g += 2) {
         const int par = (g >> 1) & 1;                           // parity of the group's steps
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g & 3], (g >> 2) & 1));
+        ok = __all_sync(0xffffffffu, tile_done_wait(sh.k_done, g));
         if (!ok) break;
         tc_fence_after();
         float x[NR];
@@ -441,7 +432,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
             }
           }
           if (g - 2 >= gs && has_o) {                           // O holds the group's steps before this one
-            ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g - 2) & 3], ((g - 2) >> 2) & 1));
+            ok = __all_sync(0xffffffffu, tile_done_wait(sh.v_done, g - 2));
             if (!ok) break;
             tc_fence_after();
             float o[NR];
@@ -450,6 +441,21 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
             for (int q = 0; q < NR; ++q) o[q] = alpha[q] == 0.f ? 0.f : o[q] * alpha[q];
             few_tmem_st<NR>(lane_base + C::kO + x2 * NQ, o);
             tmem_wait_st();
+          }
+        }
+        if (!KV8 && (k0 < w.kmin || k0 + 128 > w.len)) {
+          // This thread's row of V, if its key is one that nobody sees (behind the sequence,
+          // before the window, in a page that was not loaded), becomes zeros: its P is 0, and 0
+          // times whatever lies there has to be 0.  (e4m3: the widening warps do it.)
+          const int vst = g % C::KSV;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.v_full[vst], (g / C::KSV) & 1));
+          if (!ok) break;
+          if (key < w.kmin || key >= w.len) {
+            uint4* v = reinterpret_cast<uint4*>(m.v + vst * C::kTile + row * 128);
+#pragma unroll
+            for (int b = 0; b < C::NB; ++b)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[b * (C::kBox / 16) + i] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         // P(g) takes the buffer of P(g - NP): PV(g - NP) is done, S(g) came behind it
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
       // epilogue (group 0): both groups' sums, the last PV, then O / l and the LSE of the piece
       ok = __all_sync(0xffffffffu, mbar_wait(&sh.done[pp], (uq >> 1) & 1));
       const int glast = g_end - 1;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 3], (glast >> 2) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, tile_done_wait(sh.v_done, glast));
       if (!ok) break;
       tc_fence_after();
       float o0[NR], o1[NR];

@@ -5,9 +5,9 @@
 namespace attn {
 
 // ------------------------------------------------------------------ one query tile per CTA
-// Warps 0-7 softmax (two groups of 64 keys, thread = tile row = TMEM lane), warp 8
-// producer, warp 9 MMA issuer and, for an e4m3 cache, warps 10-17 that widen raw tiles to
-// bf16 ones.  TMEM: S in two buffers, so S of the next tile is computed while the softmax
+// Warps 0-7 softmax (two groups of 64 keys, thread = tile row = TMEM lane), warps
+// 8 and 10 producers of K (and Q) and of V, warp 9 MMA issuer and, for an e4m3 cache, warps
+// 11-18 that widen raw tiles to bf16 ones.  TMEM: S in two buffers, so S of the next tile is computed while the softmax
 // works on this one, and O.
 template <int D_, bool KV8_>
 struct RowsCfg {
@@ -22,7 +22,7 @@ struct RowsCfg {
   static constexpr int kKTile = kTile;
   static constexpr int kQTile = kTile, kQBox = kBox;
   static constexpr int kWiden = KV8 ? 8 : 0;       // widening warps
-  static constexpr int kThreads = 320 + 32 * kWiden;
+  static constexpr int kThreads = 352 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
   static constexpr int RST = KV8 ? (D == 128 ? 3 : 6) : 0;   // raw stages, K and V tiles alternating
   static constexpr int kRawMod = KV8 ? RST : 1;
@@ -42,8 +42,7 @@ struct RowsCfg {
 struct RowsShared : PagedPipe {
   float xmax[2][2][128];      // [parity of the quadrant's steps][group][row] partial row maxima
   float xsum[2][128];
-  uint64_t s_full[2], p_ready[2];
-  uint64_t pv_done[2];        // P V of step g complete, by g % 2: a waiter may be a step behind
+  uint64_t p_ready[2];
   uint64_t xbar[2][4];        // [parity][quadrant]: both groups' warps posted their maxima
   uint64_t sbar[4];
   uint64_t o_free;
@@ -63,11 +62,9 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    paged_pipe_init<C>(sh, 9 + C::kWiden, 10 + C::kWiden);
+    paged_pipe_init<C>(sh, 10 + C::kWiden, 11 + C::kWiden);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_ready[i], 8);
-      mbar_init(&sh.pv_done[i], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&sh.xbar[i][q], 2);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&sh.sbar[q], 2);
@@ -84,7 +81,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == 8) {
-    paged_produce<C>(p, sh, &tmq, &tmk, &tmv, m, cta, lane);
+    paged_produce_k<C>(p, sh, &tmq, &tmk, m, cta, lane);
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     // Per piece: S(0), S(1); then per step j: PV(j), S(j + 2) into the buffer PV(j) just
@@ -113,8 +110,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
           const uint32_t off = ((k >> 2) * C::kBox + (k & 3) * 32) >> 4;
           umma_ss_lo(tmem + ((g & 1) ? C::kS1 : C::kS0), q_lo + off, k_lo + off, hi, idS, k > 0);
         }
-        umma_commit(&sh.s_full[g & 1]);
-        umma_commit(&sh.k_empty[st]);
+        umma_commit(&sh.k_done[kc & 7]);
       }
       __syncwarp();
       ++kc;
@@ -145,8 +141,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
           for (int k2 = 0; k2 < 8; ++k2)
             umma_ts_lo(tmem + C::kO, sbase + (k2 >> 2) * 64 + (k2 & 3) * 8, v_lo + ((k2 * 2048) >> 4), hi, idO,
                        !(j == 0 && k2 == 0));
-          umma_commit(&sh.pv_done[g & 1]);
-          umma_commit(&sh.v_empty[vst]);
+          umma_commit(&sh.v_done[vc & 7]);
         }
         __syncwarp();
         if (j + 2 < w.n) {
@@ -163,8 +158,10 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 10) {
-    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 320, lane, [](int, int) {});
+  } else if (warp == 10) {
+    paged_produce_v<C>(p, sh, &tmv, m, lane);
+  } else if (warp >= 11) {
+    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 352, lane, [](int, int) {});
   } else {
     // ------------------------------------------------------------ softmax warps 0-7
     const int grp = warp >> 2;                                  // keys [64 grp, 64 grp + 64)
@@ -197,7 +194,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       for (int j = 0; j < w.n && ok; ++j) {
         const int g2 = gs + j, xp = xs & 1;
         const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 64;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g2 & 1], (g2 >> 1) & 1));
+        ok = __all_sync(0xffffffffu, tile_done_wait(sh.k_done, g2));
         if (!ok) break;
         if (!active) {
           if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
@@ -253,7 +250,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
         // S(j) was issued before PV(j - 1) (and after PV(j - 2), which its commit covers):
         // wait for PV(j - 1) before rescaling O
         if (__any_sync(0xffffffffu, need && j > 0)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g2 - 1) & 1], ((g2 - 1) >> 1) & 1));
+          ok = __all_sync(0xffffffffu, tile_done_wait(sh.v_done, g2 - 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -309,9 +306,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar[quad], uq & 1));
       if (!ok) break;
       if (active) l = sh.xsum[0][row] + sh.xsum[1][row];
-      // PV(glast): S(glast) covered PV(glast - 2), the one before it on this barrier, so the
-      // parity is unambiguous (a parity wait tells apart two successive phases only)
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
+      ok = __all_sync(0xffffffffu, tile_done_wait(sh.v_done, glast));
       if (!ok) break;
       if (active) {
         tc_fence_after();
