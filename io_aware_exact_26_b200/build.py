@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libattn_b200.so")
 SOURCES = [os.path.join(CSRC, "api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("sm100.cuh", "fwd.cuh", "fwd_pp.cuh", "bwd.cuh", "decode.cuh",
-                                              "cache.cuh", "paged.cuh", "paged_rows.cuh", "paged_few.cuh", "paged_api.cuh")] + [
+                                              "cache.cuh", "paged.cuh", "paged_rows.cuh", "paged_few.cuh", "paged_pair.cuh", "paged_api.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("attn.h", "attn_paged.h")]
 
 NVCC_FLAGS = [

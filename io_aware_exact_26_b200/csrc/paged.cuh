@@ -35,7 +35,6 @@ struct PagedParams {
   int causal, wl;             // wl < 0: no window
   float cs;                   // scale * log2(e), floored (folded_scale)
   int ctas;                   // CTAs of the launch
-  int min_tiles;              // no CTA's share is cut below this many tiles
   int slot_rows;              // rows of a workspace slot
   float* opart;               // [2 * ctas][slot_rows][D], normalised by the part's own sum
   float* lpart;               // [2 * ctas][slot_rows], natural log; -inf: no key seen
@@ -170,8 +169,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlan& pl, 
     incl = block_scan(mine, pl.warp_sum, sum);
     total += sum;
   }
-  const long long most = total / p.min_tiles;
-  const int parts = static_cast<int>(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
+  const int parts = static_cast<int>(total < 1 ? 1 : total < p.ctas ? total : p.ctas);
   const long long begin = cta < parts ? total * cta / parts : total, end = cta < parts ? total * (cta + 1) / parts : total;
   if (threadIdx.x == 0) {
     pl.total = total;
@@ -522,9 +520,11 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, PagedPipe&
         const int qs = uq % C::QST;
         if (uq >= C::QST) ok = mbar_wait(&sh.q_empty[qs], ((uq / C::QST) - 1) & 1);
         if (ok) {
-          mbar_arrive_expect_tx(&sh.q_full[qs], p.G * p.R * C::D * 2);
-          for (int c = 0; c < C::NB; ++c)
-            tma_load_3d(m.q + qs * C::kQTile + c * C::kQBox, tmq, &sh.q_full[qs], c * 64, w.g * p.G, w.tok0);
+          const int teams = C::kTeams > 1 && w.ntok > p.R ? 2 : 1;    // query tiles of the item
+          mbar_arrive_expect_tx(&sh.q_full[qs], teams * p.G * p.R * C::D * 2);
+          for (int c = 0; c < teams * C::NB; ++c)
+            tma_load_3d(m.q + qs * C::kQTile + c * C::kQBox, tmq, &sh.q_full[qs], (c % C::NB) * 64, w.g * p.G,
+                        w.tok0 + (c / C::NB) * p.R);
           ++uq;
         }
       }
@@ -684,16 +684,17 @@ __device__ __forceinline__ void paged_zero_v(const PagedSeg& w, int j, uint8_t* 
   __syncwarp();
 }
 
-// Merge of cut items: block x looks after the item whose first part CTA x holds, the
-// blocks along y share its rows; one warp per row, D / 32 columns per lane.
+// Merge of cut items: the blocks of column x look after the item whose first part CTA x
+// holds; one warp per row, D / 32 columns per lane.  The lanes first take the row's LSEs, one
+// part each, then all read the parts' O in turn, 8 of them in flight.
 template <int D>
-__global__ void __launch_bounds__(128) attn_paged_merge_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256) attn_paged_merge_kernel(const PagedParams p) {
   grid_dependency_wait();
   constexpr int PER = D / 32;
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const PagedCut cut = p.cuts[c];
   const int rows = cut.ntok * p.G;
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
     auto at = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.slot_rows + r; };
     float m = -INFINITY;
     for (int s = lane; s < cut.parts; s += 32) m = fmaxf(m, p.lpart[at(s)]);
@@ -703,14 +704,37 @@ __global__ void __launch_bounds__(128) attn_paged_merge_kernel(const PagedParams
 #pragma unroll
     for (int x = 0; x < PER; ++x) acc[x] = 0.f;
     float wsum = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < cut.parts; ++s) {
-      const float ls = p.lpart[at(s)];
-      const float w = ls == -INFINITY ? 0.f : ex2_approx((ls - m) * 1.4426950408889634f);
-      wsum += w;
-      const float* src = p.opart + at(s) * D + lane * PER;
+    for (int s0 = 0; s0 < cut.parts; s0 += 32) {
+      const float ls = s0 + lane < cut.parts ? p.lpart[at(s0 + lane)] : -INFINITY;
+      const float mine = ls == -INFINITY ? 0.f : ex2_approx((ls - m) * 1.4426950408889634f);
+      const int n = min(32, cut.parts - s0);
+      for (int t0 = 0; t0 < n; t0 += 8) {
+        float o[8][PER];
 #pragma unroll
-      for (int x = 0; x < PER; ++x) acc[x] = fmaf(w, src[x], acc[x]);
+        for (int t = 0; t < 8; ++t) {
+#pragma unroll
+          for (int x = 0; x < PER; ++x) o[t][x] = 0.f;
+          if (t0 + t < n) {
+            const float* src = p.opart + at(s0 + t0 + t) * D + lane * PER;
+            if constexpr (PER == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src);
+              o[t][0] = v.x; o[t][1] = v.y; o[t][2] = v.z; o[t][3] = v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(src);
+              o[t][0] = v.x; o[t][1] = v.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float w = __shfl_sync(0xffffffffu, mine, (t0 + t) & 31);
+          if (t0 + t < n) {
+            wsum += w;
+#pragma unroll
+            for (int x = 0; x < PER; ++x) acc[x] = fmaf(w, o[t][x], acc[x]);
+          }
+        }
+      }
     }
     const int i = r / p.G, h = r - i * p.G;
     const size_t orow = static_cast<size_t>(cut.tok0 + i) * p.Hq + cut.g * p.G + h;

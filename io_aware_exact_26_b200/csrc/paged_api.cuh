@@ -3,6 +3,7 @@
 #pragma once
 #include "attn_paged.h"
 #include "paged_few.cuh"
+#include "paged_pair.cuh"
 #include "paged_rows.cuh"
 
 namespace {
@@ -155,10 +156,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int sme
 }
 
 // Query rows per item, by the batch's mean: the smallest build of the kernel for few rows
-// that takes a sequence's rows, else 128.  Any form is right for any lengths.
-int paged_form(int T, int B, int G) {
+// that takes a sequence's rows, else 128, or 256 (two tiles, bf16 cache) where a sequence has
+// more than one tile's.  Any form is right for any lengths.
+int paged_form(int T, int B, int G, int dtype) {
   const long long rows = static_cast<long long>(G) * ((T + B - 1) / B);
-  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || dtype == ATTN_E4M3 ? 128 : 256;
 }
 
 // Workspace of the cut items: descriptors, LSE of the parts, then their O (fp32).
@@ -169,7 +171,7 @@ struct PagedWs {
 PagedWs paged_ws(int T, int G, int form, int d, int sms) {
   PagedWs w;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const long long R = form / G;
+  const long long R = form == 256 ? 2 * (128 / G) : form / G;      // tokens of an item
   w.slot_rows = static_cast<int>((T < R ? T : R) * G);
   w.l_off = up(sizeof(attn::PagedCut) * sms);
   w.o_off = up(w.l_off + static_cast<size_t>(2) * sms * w.slot_rows * 4);
@@ -202,8 +204,9 @@ int launch_paged(Kernel kernel, const void* q, const attn_strides_t* q_strides, 
     return ATTN_ERR_LAUNCH;
   if (launch_pdl(kernel, dim3(p.ctas), C::kThreads, C::kSmem, stream, tq, tk, tv, p) != cudaSuccess)
     return ATTN_ERR_LAUNCH;
-  const dim3 grid(p.ctas, (p.slot_rows + 15) / 16);
-  if (launch_pdl(attn::attn_paged_merge_kernel<C::D>, grid, 128, 0, stream, p) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  // two rows to a warp, or four of the items of two tiles, which are seldom cut in many parts
+  const dim3 grid(p.ctas, p.slot_rows <= 128 ? (p.slot_rows + 15) / 16 : (p.slot_rows + 31) / 32);
+  if (launch_pdl(attn::attn_paged_merge_kernel<C::D>, grid, 256, 0, stream, p) != cudaSuccess) return ATTN_ERR_LAUNCH;
   return ATTN_OK;
 }
 
@@ -218,6 +221,10 @@ int launch_paged_form(int form, const void* q, const attn_strides_t* q_strides, 
   ATTN_FEW(16)
   ATTN_FEW(32)
 #undef ATTN_FEW
+  if constexpr (!KV8) {
+    if (form == 256)
+      return launch_paged<attn::PairCfg<D>>(attn::attn_paged_pair_kernel<D>, q, q_strides, cache, p, s);
+  }
   return launch_paged<attn::RowsCfg<D, KV8>>(attn::attn_paged_rows_kernel<D, KV8>, q, q_strides, cache, p, s);
 }
 
@@ -364,7 +371,11 @@ size_t attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d) {
   if (check_paged_heads(T, B, Hq, Hkv, d) != ATTN_OK || T == 0) return 0;
   DeviceInfo* di = nullptr;
   if (device_info(&di) != 0) return 0;
-  return paged_ws(T, Hq / Hkv, paged_form(T, B, Hq / Hkv), d, di->sms).total;
+  // enough for either cache type
+  const int G = Hq / Hkv;
+  const size_t a = paged_ws(T, G, paged_form(T, B, G, ATTN_BF16), d, di->sms).total;
+  const size_t b = paged_ws(T, G, paged_form(T, B, G, ATTN_E4M3), d, di->sms).total;
+  return a > b ? a : b;
 }
 
 int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache, const attn_batch_t* batch,
@@ -382,7 +393,7 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   DeviceInfo* di = nullptr;
   if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
   const int d = cache->d, G = Hq / cache->Hkv;
-  const int form = paged_form(batch->T, batch->B, G);
+  const int form = paged_form(batch->T, batch->B, G, cache->dtype);
   const PagedWs W = paged_ws(batch->T, G, form, d, di->sms);
   if (workspace && workspace_bytes < W.total) return ATTN_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -404,13 +415,12 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   p.Hq = Hq;
   p.Hkv = cache->Hkv;
   p.G = G;
-  p.R = form / G;
-  p.RI = p.R;
+  p.R = (form == 256 ? 128 : form) / G;
+  p.RI = form == 256 ? 2 * p.R : p.R;
   p.causal = causal;
   p.wl = window_left < 0 ? -1 : window_left;
   p.cs = attn::folded_scale(scale);
   p.ctas = di->sms;
-  p.min_tiles = 1;
   p.slot_rows = W.slot_rows;
   p.cuts = static_cast<attn::PagedCut*>(ws);
   p.lpart = reinterpret_cast<float*>(static_cast<char*>(ws) + W.l_off);

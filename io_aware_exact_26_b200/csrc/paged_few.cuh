@@ -47,6 +47,7 @@ struct FewCfg {
   static constexpr int NQ = NR < 16 ? 16 : NR;     // columns of S^T and O^T
   static constexpr bool KV8 = KV8_, K8 = KV8_;
   static constexpr int kTile = 128 * D * 2;        // bf16 tile
+  static constexpr int kTeams = 1;
   static constexpr int kBox = 128 * 128;
   static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
   static constexpr int kKTile = K8 ? 128 * 128 : kTile;

@@ -14,6 +14,7 @@ struct RowsCfg {
   static constexpr int D = D_;
   static constexpr bool KV8 = KV8_;
   static constexpr int kTile = 128 * D * 2;
+  static constexpr int kTeams = 1;
   static constexpr int kBox = 128 * 128;
   static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
   static constexpr int QST = (KV8 && D == 128) ? 1 : 2;

@@ -57,57 +57,61 @@ def declare(L):
 
 
 _same_device = contextlib.nullcontext()
+_bf16, _f32, _i32, _e4m3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 
-def _on(device):
-    """Context with ``device`` current (nothing to do where it is already)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return _same_device
-    return torch.cuda.device(device)
+def _on(index):
+    """Context with device ``index`` current (nothing to do where it is already)."""
+    return _same_device if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _stream(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)       # torch.cuda.current_stream, without the object
 
 
-def _tensor(t, name, dtype, device=None, dim=None, contiguous=False):
+def _tensor(t, name, dtype, index=None, dim=None, contiguous=False):
+    """Raise unless t is such a tensor; a decoding step checks a dozen, so the good case is one
+    expression."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and (index is None or t.get_device() == index)
+            and (dim is None or t.dim() == dim) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call on {device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{index}")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
     if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
-def _unit(t, dim):
-    # the stride of a dimension of one entry is never followed; torch may report anything
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+def _strides(t):
+    """Strides of a packed [T, H, d] or dense [B, H, N, d] tensor.  The stride of a dimension of
+    one entry is never followed and may be anything in torch: zero here."""
+    st, sh = t.stride(), t.shape
+    if len(sh) == 3:
+        return _Strides(0, st[1] if sh[1] > 1 else 0, st[0] if sh[0] > 1 else 0)
+    return _Strides(st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0, st[2] if sh[2] > 1 else 0)
 
 
-def _packed(t):
-    return _Strides(0, _unit(t, 1), _unit(t, 0))
+_no_strides = _Strides()
 
 
-def _dense(t):
-    return _Strides(_unit(t, 0), _unit(t, 1), _unit(t, 2))
+def _rope_struct(inv_freq, interleaved, mscale, index):
+    _tensor(inv_freq, "inv_freq", torch.float64, index, 1, contiguous=True)
+    return _Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, mscale)
 
 
-def _rope_struct(inv_freq, interleaved, mscale, device):
-    _tensor(inv_freq, "inv_freq", torch.float64, device, 1, contiguous=True)
-    return _Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)), float(mscale))
-
-
-def _check_out(out, like, name, device):
-    _tensor(out, name, like.dtype, device)
+def _check_out(out, like, name, index):
+    _tensor(out, name, like.dtype, index)
     if out.shape != like.shape:
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(out.shape)}")
 
@@ -152,49 +156,45 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original=None,
 
 
 def _rope_call(name, inverse, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out, stream):
-    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(q, torch.Tensor) or (q.dtype is not _bf16 and q.dtype is not _f32):
         raise TypeError("q must be a bfloat16 or float32 tensor")
-    _tensor(q, "q", q.dtype)
-    dev = q.device
-    if q.dim() not in (3, 4):
+    dt = q.dtype
+    _tensor(q, "q", dt)
+    dev = q.get_device()
+    sh = q.shape
+    if len(sh) == 4:
+        B, Hq, N, d = sh
+    elif len(sh) == 3:
+        (N, Hq, d), B = sh, 1
+    else:
         raise ValueError("q must be [B, H, N, d] or [T, H, d]")
-    dense = q.dim() == 4
-    if dense:
-        B, Hq, N, d = q.shape
-    else:
-        (N, Hq, d), B = q.shape, 1
-    Hkv = 0
+    Hkv, kp, kop, ks, kos = 0, None, None, _no_strides, _no_strides
     if k is not None:
-        _tensor(k, "k", q.dtype, dev, q.dim())
+        _tensor(k, "k", dt, dev, len(sh))
         Hkv = k.shape[1]
-        if k.shape != ((B, Hkv, N, d) if dense else (N, Hkv, d)):
+        if k.shape != ((B, Hkv, N, d) if len(sh) == 4 else (N, Hkv, d)):
             raise ValueError("k must have q's shape apart from the number of heads")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    _tensor(positions, "positions", torch.int32, dev)
-    if tuple(positions.shape) not in (((N,), (B, N)) if dense else ((N,),)):
-        raise ValueError("positions must have one entry per token: [N], or [B, N] for dense tensors")
-    if not positions.is_contiguous():
-        raise ValueError("positions must be contiguous")
-    rope = _rope_struct(inv_freq, interleaved, mscale, dev)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _check_out(q_out, q, "q_out", dev)
-    if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            k_out = k.new_empty(k.shape)
         else:
             _check_out(k_out, k, "k_out", dev)
-    st = _dense if dense else _packed
-    none = _Strides()
+        kp, kop, ks, kos = k.data_ptr(), k_out.data_ptr(), _strides(k), _strides(k_out)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _tensor(positions, "positions", _i32, dev, contiguous=True)
+    per_batch = positions.dim() == 2
+    if positions.shape != ((B, N) if per_batch and len(sh) == 4 else (N,)):
+        raise ValueError("positions must have one entry per token: [N], or [B, N] for dense tensors")
+    rope = _rope_struct(inv_freq, interleaved, mscale, dev)
+    if q_out is None:
+        q_out = q.new_empty(sh)
+    else:
+        _check_out(q_out, q, "q_out", dev)
     with _on(dev):
         rc = binding.lib().attn_rope(
-            q.data_ptr(), st(q), q_out.data_ptr(), st(q_out), Hq,
-            k.data_ptr() if k is not None else None, st(k) if k is not None else none,
-            k_out.data_ptr() if k is not None else None, st(k_out) if k is not None else none, Hkv,
-            _BF16 if q.dtype == torch.bfloat16 else _F32, B, N, d, positions.data_ptr(),
-            N if positions.dim() == 2 else 0, rope, inverse, _stream(stream, dev))
+            q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out), Hq, kp, ks, kop, kos, Hkv,
+            _BF16 if dt is _bf16 else _F32, B, N, d, positions.data_ptr(), N if per_batch else 0, rope, inverse,
+            _stream(stream, dev))
     if rc != ATTN_OK:
         raise AttnError(rc, name)
     return q_out, k_out
@@ -220,45 +220,52 @@ def attn_rope_bwd(dq, dk=None, *, positions, inv_freq, interleaved=False, mscale
 
 
 def _cache_struct(k_cache, v_cache, k_scale, v_scale):
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    if not isinstance(k_cache, torch.Tensor) or (k_cache.dtype is not _bf16 and k_cache.dtype is not _e4m3):
         raise TypeError("k_cache must be a bfloat16 or float8_e4m3fn tensor")
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    _tensor(k_cache, "k_cache", k_cache.dtype, None, 4)
-    dev = k_cache.device
-    _tensor(v_cache, "v_cache", k_cache.dtype, dev, 4)
-    if v_cache.shape != k_cache.shape:
+    dt = k_cache.dtype
+    _tensor(k_cache, "k_cache", dt, None, 4)
+    dev = k_cache.get_device()
+    _tensor(v_cache, "v_cache", dt, dev, 4)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape, [num_pages, Hkv, page_size, d]")
-    pages, Hkv, page, d = k_cache.shape
-    full = Hkv * page * d
-    stride = k_cache.stride(0) if pages > 1 else full
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if (Hkv > 1 and t.stride(1) != page * d) or (page > 1 and t.stride(2) != d):
-            raise ValueError(f"{n}: a page must be contiguous")
-        if pages > 1 and t.stride(0) != stride:
-            raise ValueError("k_cache and v_cache must have one page stride")
-    if e4m3:
+    pages, Hkv, page, d = shape
+    stride = Hkv * page * d
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        if pages > 1:
+            stride = k_cache.stride(0)
+            if v_cache.stride(0) != stride:
+                raise ValueError("k_cache and v_cache must have one page stride")
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if (Hkv > 1 and t.stride(1) != page * d) or (page > 1 and t.stride(2) != d):
+                raise ValueError(f"{n}: a page must be contiguous")
+    ks = vs = None
+    if dt is _e4m3:
         for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _tensor(t, n, torch.uint8, dev, 3, contiguous=True)
-            if t.shape != k_cache.shape[:3]:
+            if t.shape != shape[:3]:
                 raise ValueError(f"{n} must be [num_pages, Hkv, page_size]")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("a bfloat16 cache has no scales")
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if e4m3 else None,
-                  v_scale.data_ptr() if e4m3 else None, stride, pages, page, Hkv, d, _E4M3 if e4m3 else _BF16), dev
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, stride, pages, page, Hkv, d,
+                  _E4M3 if dt is _e4m3 else _BF16), dev, Hkv, d
 
 
 def _batch_struct(block_table, cu_q, kv_len, T, dev):
-    _tensor(block_table, "block_table", torch.int32, dev, 2, contiguous=True)
-    _tensor(kv_len, "kv_len", torch.int32, dev, 1, contiguous=True)
+    _tensor(block_table, "block_table", _i32, dev, 2, contiguous=True)
+    _tensor(kv_len, "kv_len", _i32, dev, 1, contiguous=True)
     B = kv_len.shape[0]
-    if block_table.shape[0] != B:
+    rows, width = block_table.shape
+    if rows != B:
         raise ValueError("block_table must have a row per sequence")
+    cu = None
     if cu_q is not None:
-        _tensor(cu_q, "cu_q", torch.int32, dev, 1, contiguous=True)
+        _tensor(cu_q, "cu_q", _i32, dev, 1, contiguous=True)
         if cu_q.shape[0] != B + 1:
             raise ValueError("cu_q must have one entry more than kv_len")
-    return _Batch(cu_q.data_ptr() if cu_q is not None else None, kv_len.data_ptr(), block_table.data_ptr(), B, T,
-                  block_table.shape[1])
+        cu = cu_q.data_ptr()
+    return _Batch(cu, kv_len.data_ptr(), block_table.data_ptr(), B, T, width)
 
 
 def attn_cache_write(k, v, k_cache, v_cache, block_table, cu_q, kv_len, *, k_scale=None, v_scale=None, inv_freq=None,
@@ -272,36 +279,32 @@ def attn_cache_write(k, v, k_cache, v_cache, block_table, cu_q, kv_len, *, k_sca
     is q [T, Hq, d] if given, into q_out (allocated if None; may be q), all in one launch.
     Returns q_out (None without q).
     """
-    cache, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale)
-    Hkv, d = cache.Hkv, cache.d
-    _tensor(k, "k", torch.bfloat16, dev, 3)
-    _tensor(v, "v", torch.bfloat16, dev, 3)
+    cache, dev, Hkv, d = _cache_struct(k_cache, v_cache, k_scale, v_scale)
+    _tensor(k, "k", _bf16, dev, 3)
+    _tensor(v, "v", _bf16, dev, 3)
     T = k.shape[0]
     if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
         raise ValueError("k and v must be [T, Hkv, d] with the cache's heads and head size")
     batch = _batch_struct(block_table, cu_q, kv_len, T, dev)
     rope = None if inv_freq is None else _rope_struct(inv_freq, interleaved, mscale, dev)
-    Hq = 0
+    Hq, qp, qop, qs, qos = 0, None, None, _no_strides, _no_strides
     if q is not None:
         if rope is None:
             raise ValueError("q is rotated only: give inv_freq")
-        _tensor(q, "q", torch.bfloat16, dev, 3)
+        _tensor(q, "q", _bf16, dev, 3)
         Hq = q.shape[1]
         if q.shape != (T, Hq, d):
             raise ValueError("q must be [T, Hq, d]")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = q.new_empty(q.shape)
         else:
             _check_out(q_out, q, "q_out", dev)
+        qp, qop, qs, qos = q.data_ptr(), q_out.data_ptr(), _strides(q), _strides(q_out)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    none = _Strides()
     with _on(dev):
-        rc = binding.lib().attn_cache_write(
-            cache, batch, k.data_ptr(), _packed(k), v.data_ptr(), _packed(v), rope,
-            q.data_ptr() if q is not None else None, _packed(q) if q is not None else none,
-            q_out.data_ptr() if q is not None else None, _packed(q_out) if q is not None else none, Hq,
-            _stream(stream, dev))
+        rc = binding.lib().attn_cache_write(cache, batch, k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), rope,
+                                            qp, qs, qop, qos, Hq, _stream(stream, dev))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_write")
     return q_out
@@ -315,19 +318,19 @@ def attn_cache_read(k_cache, v_cache, block_table, kv_len, *, k_scale=None, v_sc
     Rows behind a sequence's length keep what k_out and v_out hold (zeros where they are
     allocated here, which needs N).
     """
-    cache, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale)
+    cache, dev, Hkv, d = _cache_struct(k_cache, v_cache, k_scale, v_scale)
     batch = _batch_struct(block_table, None, kv_len, 0, dev)
     if N is None:
         if k_out is None:
             raise ValueError("give N or k_out and v_out")
         N = k_out.shape[2]
-    shape = (batch.B, cache.Hkv, int(N), cache.d)
+    shape = (batch.B, Hkv, int(N), d)
     if k_out is None:
-        k_out = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+        k_out = kv_len.new_zeros(shape, dtype=_bf16)
     if v_out is None:
-        v_out = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+        v_out = kv_len.new_zeros(shape, dtype=_bf16)
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _tensor(t, n, torch.bfloat16, dev, 4, contiguous=True)
+        _tensor(t, n, _bf16, dev, 4, contiguous=True)
         if t.shape != shape:
             raise ValueError(f"{n} must have shape {shape}")
     with _on(dev):
@@ -353,31 +356,33 @@ def attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *, k_scale=None, 
     workspace: a device tensor of attn_paged_workspace_size(T, B, Hq, Hkv, d) bytes, one for
     each call that may run at the same time; None lets the library allocate it on the stream.
     """
-    cache, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale)
-    _tensor(q, "q", torch.bfloat16, dev, 3)
+    cache, dev, _, dc = _cache_struct(k_cache, v_cache, k_scale, v_scale)
+    _tensor(q, "q", _bf16, dev, 3)
     T, Hq, d = q.shape
-    if d != cache.d:
+    if d != dc:
         raise ValueError("q and the cache differ in head size")
     batch = _batch_struct(block_table, cu_q, kv_len, T, dev)
     if o is None:
-        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        o = q.new_empty((T, Hq, d))
+    else:
+        _tensor(o, "o", _bf16, dev, 3, contiguous=True)
+        if o.shape != (T, Hq, d):
+            raise ValueError("o must be [T, Hq, d]")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    _tensor(o, "o", torch.bfloat16, dev, 3, contiguous=True)
-    _tensor(lse, "lse", torch.float32, dev, 2, contiguous=True)
-    if o.shape != (T, Hq, d) or lse.shape != (T, Hq):
-        raise ValueError("o must be [T, Hq, d] and lse [T, Hq]")
-    ws_bytes = 0
+        lse = q.new_empty((T, Hq), dtype=_f32)
+    else:
+        _tensor(lse, "lse", _f32, dev, 2, contiguous=True)
+        if lse.shape != (T, Hq):
+            raise ValueError("lse must be [T, Hq]")
+    ws, ws_bytes = None, 0
     if workspace is not None:
-        if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous and on the call's device")
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     with _on(dev):
-        rc = binding.lib().attn_paged(
-            q.data_ptr(), _packed(q), cache, batch, o.data_ptr(), lse.data_ptr(), Hq,
-            d ** -0.5 if scale is None else float(scale), int(bool(causal)),
-            -1 if window_left is None else int(window_left),
-            workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream, dev))
+        rc = binding.lib().attn_paged(q.data_ptr(), _strides(q), cache, batch, o.data_ptr(), lse.data_ptr(), Hq,
+                                      d ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                      -1 if window_left is None else window_left, ws, ws_bytes, _stream(stream, dev))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_paged")
     return o, lse

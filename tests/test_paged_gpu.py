@@ -394,11 +394,11 @@ def test_paged_attention_matches_the_definition(attn, case, checks):
     check_attention(*run_paged(attn, case, seed=sum(case[5]) + case[2], checks=checks))
 
 
-def ragged(B, seed):
+def ragged(B, seed, most=90):
     """Ragged batch whose tiles outnumber the SMs several times, so that every CTA works on several
     items of very different row counts, one after the other."""
     g = torch.Generator().manual_seed(seed)
-    new = [int(n) for n in torch.randint(0, 90, (B,), generator=g)]
+    new = [int(n) for n in torch.randint(0, most, (B,), generator=g)]
     new[1::3] = [1] * len(new[1::3])
     return new, [n + int(x) for n, x in zip(new, torch.randint(0, 700, (B,), generator=g))]
 
@@ -408,6 +408,31 @@ def ragged(B, seed):
 def test_paged_attention_of_many_ragged_items(attn, Hq, Hkv, d, page, e4m3, window):
     new, lens = ragged(48, seed=Hq + d)
     check_attention(*run_paged(attn, (Hq, Hkv, d, page, e4m3, new, lens, True, window), seed=d))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page,e4m3,window", [(8, 2, 128, 64, False, None), (6, 2, 64, 16, False, 150),
+                                                       (4, 4, 128, 128, False, None), (5, 1, 64, 32, True, None)])
+def test_paged_attention_of_ragged_chunks(attn, Hq, Hkv, d, page, e4m3, window):
+    """Chunks of up to several query tiles beside single tokens and empty ones."""
+    new, lens = ragged(20, seed=Hq * d, most=420)
+    check_attention(*run_paged(attn, (Hq, Hkv, d, page, e4m3, new, lens, True, window), seed=d))
+
+
+@pytest.mark.parametrize("Hq", [4, 8, 12, 32, 64])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_paged_attention_is_repeatable(attn, Hq, e4m3):
+    """Every form of the kernel, many pieces per SM: 40 launches in a row give the same bits."""
+    B, Hkv, d, page, L = 24, 2, 64 if e4m3 else 128, 16, 3000
+    lens = [L - 57 * b for b in range(B)]
+    pool = Pool(B, Hkv, page, d, lens, e4m3, seed=Hq)
+    where, scales = pool.cuda()
+    new = [1 + 3 * (b % 2) if Hq < 64 else 4 for b in range(B)]
+    q = normal((sum(new), Hq, d), Hq).cuda()
+    args = (q, *where, bounds(new).cuda(), ints(lens).cuda())
+    o, lse = attn.attn_paged(*args, **scales)
+    again = [attn.attn_paged(*args, **scales) for _ in range(40)]
+    ok(attn)
+    assert all(torch.equal(a, o) and torch.equal(b, lse) for a, b in again)
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
