@@ -132,14 +132,66 @@ struct PagedPlan {
   int b;
 };
 
-// Block-wide inclusive scan of v; returns this thread's prefix, total in all threads.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sum, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+__device__ __forceinline__ long long paged_tiles(const PagedParams& p, int b) {
+  if (b >= p.B) return 0;
+  PagedSeq s;
+  s.load(p, b);
+  return s.tiles(p) * p.Hkv;
+}
+
+// 64-bit quotient; most are of small numbers, for which 32-bit division is several times
+// faster.
+__device__ __forceinline__ long long small_div(long long a, long long b) {
+  if ((static_cast<unsigned long long>(a) | static_cast<unsigned long long>(b)) >> 32) return a / b;
+  return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+}
+
+// The CTA's range of W tiles.
+__device__ __forceinline__ void paged_share(const PagedParams& p, int cta, long long total, int& parts, long long& begin,
+                                            long long& end) {
+  parts = static_cast<int>(total < 1 ? 1 : total < p.ctas ? total : p.ctas);
+  begin = cta < parts ? small_div(total * cta, parts) : total;
+  end = cta < parts ? small_div(total * (cta + 1), parts) : total;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long w = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += w;
   }
+  return v;
+}
+
+// The plan by one warp, for at most 32 sequences.
+__device__ __forceinline__ void paged_plan_warp(const PagedParams& p, PagedPlan& pl, int cta, int lane) {
+  const long long mine = paged_tiles(p, lane);
+  const long long incl = warp_scan(mine, lane);
+  const long long total = __shfl_sync(0xffffffffu, incl, 31);
+  int parts;
+  long long begin, end;
+  paged_share(p, cta, total, parts, begin, end);
+  if (lane == 0) {
+    pl.total = total;
+    pl.parts = parts;
+    pl.begin = begin;
+    pl.end = end;
+    pl.b = p.B;
+  }
+  __syncwarp();
+  const long long from = incl - mine;
+  if (begin < end && from <= begin && begin < from + mine) {
+    pl.b = lane;
+    pl.rest = begin - from;
+    pl.head_tiles = small_div(mine, p.Hkv);
+  }
+  __syncwarp();
+}
+
+// Block-wide inclusive scan of v; returns this thread's prefix, total in all threads.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sum, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  v = warp_scan(v, lane);
   __syncthreads();                            // warp_sum is free again
   if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
@@ -153,51 +205,48 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return before + v;
 }
 
-// All threads of the CTA: W, the CTA's range and the sequence it begins in.
-__device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlan& pl, int cta) {
+// The plan by all threads of the CTA, for any number of sequences.
+__device__ __forceinline__ void paged_plan_block(const PagedParams& p, PagedPlan& pl, int cta) {
   const int nt = blockDim.x;
   long long mine = 0, incl = 0, total = 0, sum = 0;
   if (threadIdx.x == 0) pl.b = p.B;           // nothing found yet; the scan's barriers order this first
   for (int b0 = 0; b0 < p.B; b0 += nt) {
-    const int b = b0 + threadIdx.x;
-    mine = 0;
-    if (b < p.B) {
-      PagedSeq s;
-      s.load(p, b);
-      mine = s.tiles(p) * p.Hkv;
-    }
+    mine = paged_tiles(p, b0 + threadIdx.x);
     incl = block_scan(mine, pl.warp_sum, sum);
     total += sum;
   }
-  const int parts = static_cast<int>(total < 1 ? 1 : total < p.ctas ? total : p.ctas);
-  const long long begin = cta < parts ? total * cta / parts : total, end = cta < parts ? total * (cta + 1) / parts : total;
+  int parts;
+  long long begin, end, base = 0;
+  paged_share(p, cta, total, parts, begin, end);
   if (threadIdx.x == 0) {
     pl.total = total;
     pl.parts = parts;
     pl.begin = begin;
     pl.end = end;
   }
-  long long base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += nt) {      // again, to find the sequence that holds tile `begin`
+  for (int b0 = 0; b0 < p.B; b0 += nt) {      // find the sequence that holds tile `begin`
     const int b = b0 + threadIdx.x;
     if (p.B > nt) {
-      mine = 0;
-      if (b < p.B) {
-        PagedSeq s;
-        s.load(p, b);
-        mine = s.tiles(p) * p.Hkv;
-      }
+      mine = paged_tiles(p, b);
       incl = block_scan(mine, pl.warp_sum, sum);
     }
     const long long from = base + incl - mine;
     if (b < p.B && begin < end && from <= begin && begin < from + mine) {
       pl.b = b;
       pl.rest = begin - from;
-      pl.head_tiles = mine / p.Hkv;
+      pl.head_tiles = small_div(mine, p.Hkv);
     }
     base += sum;
   }
   __syncthreads();
+}
+
+// W, the CTA's range and the sequence it begins in.  Up to 32 sequences, `planner` (the warp
+// that walks through the share) finds them alone while the others set up barriers and TMEM;
+// beyond, all threads do.
+__device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlan& pl, int cta, bool planner, int lane) {
+  if (p.B > 32) paged_plan_block(p, pl, cta);
+  else if (planner) paged_plan_warp(p, pl, cta, lane);
 }
 
 // The pieces of a CTA's share, in order.  Used by one whole warp (the first place needs
@@ -207,13 +256,14 @@ struct PagedWalk {
   int b, g, i;                // sequence, KV head, item
   int skip;                   // tiles of the item that lie before the share
   long long left;             // tiles still to hand out
+  long long cut_end = 0;      // of the item cut at the end of the share: the tile behind its last one
   __device__ __forceinline__ void begin(const PagedParams& p, const PagedPlan& pl, int lane) {
     left = pl.end - pl.begin;
     b = pl.b;
     g = i = skip = 0;
     if (left <= 0 || b >= p.B) { left = 0; return; }
     s.load(p, b);
-    g = static_cast<int>(pl.rest / pl.head_tiles);
+    g = static_cast<int>(small_div(pl.rest, pl.head_tiles));
     const long long rest = pl.rest - g * pl.head_tiles;
     int lo = 0, hi = s.nblk;                  // before(lo) <= rest < before(hi)
     while (hi - lo > 1) {
@@ -253,21 +303,26 @@ struct PagedWalk {
     w.n = static_cast<int>(left < have ? left : have);
     if (skip > 0) w.slot = 2 * cta;
     else if (w.n < n) w.slot = 2 * cta + 1;
-    if (skip == 0 && w.n < n) {               // the first part of a cut item
-      const long long last = pl.end - left + n - 1;          // the item's last tile
-      const int c1 = static_cast<int>(((last + 1) * pl.parts - 1) / pl.total);
-      PagedCut& cut = p.cuts[cta];
-      cut.tok0 = w.tok0;
-      cut.ntok = w.ntok;
-      cut.g = g;
-      cut.parts = c1 - cta + 1;
-    }
+    if (skip == 0 && w.n < n) cut_end = pl.end - left + n;   // the first part of a cut item
     left -= w.n;
     skip = 0;
     ++i;
     return w;
   }
 };
+
+// Descriptor of the item that the CTA's share cuts (one thread, once the share is walked
+// through): w is the last piece, which holds the item's first part if `walk` says so.
+__device__ __forceinline__ void paged_post_cut(const PagedParams& p, const PagedPlan& pl, const PagedWalk& walk,
+                                               const PagedSeg& w, int cta) {
+  PagedCut cut = {0, 0, 0, 0};
+  if (walk.cut_end > 0) {
+    // CTA c holds the tiles [W c / C, W (c+1) / C): the one with tile x is ((x + 1) C - 1) / W
+    const int c1 = static_cast<int>(small_div(walk.cut_end * pl.parts - 1, pl.total));
+    cut = {w.tok0, w.ntok, w.g, c1 - cta + 1};
+  }
+  p.cuts[cta] = cut;
+}
 
 // Pieces passed from the producer warp to the consumer warps, in order.
 struct SegRing {
@@ -503,17 +558,15 @@ __device__ __forceinline__ void paged_drain_tiles(PagedPipe& sh, int kc, int lan
 template <class C>
 __device__ __forceinline__ void paged_produce_k(const PagedParams& p, PagedPipe& sh, const CUtensorMap* tmq,
                                                 const CUtensorMap* tmk, const PagedSmem& m, int cta, int lane) {
-  if (lane == 0) {
-    tma_prefetch_desc(tmq); tma_prefetch_desc(tmk);
-    p.cuts[cta].ntok = 0;
-  }
-  __syncwarp();
+  if (lane == 0) { tma_prefetch_desc(tmq); tma_prefetch_desc(tmk); }
   PagedWalk walk;
   walk.begin(p, sh.plan, lane);
   int kc = 0, uq = 0;                               // key tiles, pieces
   bool ok = true;
+  PagedSeg last;
   for (int k = 0; ok; ++k) {
     const PagedSeg w = walk.next(p, sh.plan, cta);
+    if (w.n > 0) last = w;
     if (lane == 0) {
       ok = seg_ring_post(sh.ring, k, w);
       if (ok && w.n > 0) {
@@ -533,6 +586,7 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, PagedPipe&
     if (!ok || w.n == 0) break;
     ok = paged_load_tiles<C, 0>(p, sh, tmk, m, w, kc, lane);
   }
+  if (lane == 0) paged_post_cut(p, sh.plan, walk, last, cta);
   if (!ok) {
     paged_drain_tiles<C, 0>(sh, kc, lane);
     if (lane == 0)

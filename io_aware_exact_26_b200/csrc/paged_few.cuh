@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
   if (warp == 0) { tmem_alloc(&sh.tmem_base, C::kTmemCols); tmem_relinquish(); }
   grid_dependency_wait();
   grid_dependency_launch();
-  paged_plan(p, sh.plan, cta);
+  paged_plan(p, sh.plan, cta, warp == 8, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
   if (warp == 0) { tmem_alloc(&sh.tmem_base, C::kTmemCols); tmem_relinquish(); }
   grid_dependency_wait();
   grid_dependency_launch();
-  paged_plan(p, sh.plan, cta);
+  paged_plan(p, sh.plan, cta, warp == 16, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

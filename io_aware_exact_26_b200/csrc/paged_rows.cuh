@@ -25,7 +25,10 @@ struct RowsCfg {
   static constexpr int kWiden = KV8 ? 8 : 0;       // widening warps
   static constexpr int kThreads = 352 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
-  static constexpr int RST = KV8 ? (D == 128 ? 3 : 6) : 0;   // raw stages, K and V tiles alternating
+  // Raw stages, K and V tiles alternating.  An even number: the two producers run on their
+  // own, so each needs its own stages (with 3, K could take one that V had yet to fill).
+  static constexpr int RST = KV8 ? (D == 128 ? 2 : 6) : 0;
+  static_assert(RST % 2 == 0, "K and V must not share a raw stage");
   static constexpr int kRawMod = KV8 ? RST : 1;
   static constexpr int kS0 = 0, kS1 = 128, kO = 256;
   static constexpr int kTmemCols = 512;
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
   if (warp == 0) { tmem_alloc(&sh.tmem_base, C::kTmemCols); tmem_relinquish(); }
   grid_dependency_wait();
   grid_dependency_launch();
-  paged_plan(p, sh.plan, cta);
+  paged_plan(p, sh.plan, cta, warp == 8, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -411,7 +411,8 @@ def test_paged_attention_of_many_ragged_items(attn, Hq, Hkv, d, page, e4m3, wind
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,page,e4m3,window", [(8, 2, 128, 64, False, None), (6, 2, 64, 16, False, 150),
-                                                       (4, 4, 128, 128, False, None), (5, 1, 64, 32, True, None)])
+                                                       (4, 4, 128, 128, False, None), (5, 1, 64, 32, True, None),
+                                                       (6, 2, 128, 16, True, None), (8, 8, 128, 64, True, 300)])
 def test_paged_attention_of_ragged_chunks(attn, Hq, Hkv, d, page, e4m3, window):
     """Chunks of up to several query tiles beside single tokens and empty ones."""
     new, lens = ragged(20, seed=Hq * d, most=420)
