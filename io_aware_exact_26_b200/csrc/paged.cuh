@@ -365,11 +365,6 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* tmap, ui
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
-// Programmatic dependent launch: wait until the kernels before this one have finished and
-// their writes are visible / let the next kernel's blocks start early.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ------------------------------------------------------------------ pipeline shared by the kernels
 // Barriers between the producer warp, the widening warps (e4m3 cache) and the MMA warp.
 struct PagedPipe {

@@ -64,6 +64,23 @@ attn::CacheView cache_view(const attn_cache_t* c) {
   return v;
 }
 
+// Launch with programmatic stream serialisation: the kernel may be set up while the one
+// before it runs, and waits for it on the device (griddepcontrol.wait).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Heads that one block walks through: all of them where the tokens alone fill the GPU
 // (sine and cosine are then formed once per token), else few enough that the blocks do.
 int heads_per_block(long long token_blocks, int heads, int sms) {
@@ -74,31 +91,31 @@ int heads_per_block(long long token_blocks, int heads, int sms) {
 }
 
 template <typename T, int D, bool INTER>
-void launch_rope(const attn::RopeParams& p0, int sms, cudaStream_t s) {
+cudaError_t launch_rope(const attn::RopeParams& p0, int sms, cudaStream_t s) {
   attn::RopeParams p = p0;
   constexpr int tpb = 256 / attn::RopeUnit<T, D, INTER>::kUnits;
   const long long tb = (static_cast<long long>(p.B) * p.N + tpb - 1) / tpb;
   p.heads_per_block = heads_per_block(tb, p.Hq + p.Hk, sms);
   const dim3 grid(static_cast<unsigned>(tb), (p.Hq + p.Hk + p.heads_per_block - 1) / p.heads_per_block);
-  attn::attn_rope_kernel<T, D, INTER><<<grid, 256, 0, s>>>(p);
+  return launch_pdl(attn::attn_rope_kernel<T, D, INTER>, grid, 256, 0, s, p);
 }
 
 template <int D, bool E4M3, bool INTER>
-void launch_cache_write(const attn::WriteParams& p0, int sms, cudaStream_t s) {
+cudaError_t launch_cache_write(const attn::WriteParams& p0, int sms, cudaStream_t s) {
   attn::WriteParams p = p0;
   constexpr int tpb = 256 / attn::RopeUnit<__nv_bfloat16, D, INTER>::kUnits;
   const long long tb = (static_cast<long long>(p.T) + tpb - 1) / tpb;
   const int heads = p.Hq + 2 * p.c.Hkv;
   p.heads_per_block = heads_per_block(tb, heads, sms);
   const dim3 grid(static_cast<unsigned>(tb), (heads + p.heads_per_block - 1) / p.heads_per_block);
-  attn::attn_cache_write_kernel<D, E4M3, INTER><<<grid, 256, 0, s>>>(p);
+  return launch_pdl(attn::attn_cache_write_kernel<D, E4M3, INTER>, grid, 256, 0, s, p);
 }
 
 template <int D, bool E4M3>
-void launch_cache_read(const attn::ReadParams& p, int B, cudaStream_t s) {
-  constexpr int rows = 256 / (D / 8) * 4;
+cudaError_t launch_cache_read(const attn::ReadParams& p, int B, cudaStream_t s) {
+  constexpr int rows = 256 / (D / 8) * 2;
   const dim3 grid((p.N + rows - 1) / rows, static_cast<unsigned>(B * p.c.Hkv));
-  attn::attn_cache_read_kernel<D, E4M3><<<grid, 256, 0, s>>>(p);
+  return launch_pdl(attn::attn_cache_read_kernel<D, E4M3>, grid, 256, 0, s, p);
 }
 
 // [num_pages][Hkv][page_size][d] as a 4-D map; one box is a page's (or 128 rows of it)
@@ -136,23 +153,6 @@ bool make_q_map(CUtensorMap* m, const void* q, const attn_strides_t* st, int T, 
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Launch with programmatic stream serialisation: the kernel may be set up while the one
-// before it runs, and waits for it on the device (griddepcontrol.wait).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Query rows per item, by the batch's mean: the smallest build of the kernel for few rows
@@ -273,17 +273,13 @@ int attn_rope(const void* q, const attn_strides_t* q_strides, void* q_out, const
   auto go = [&](auto tag, auto dim) {
     using T = decltype(tag);
     constexpr int D = decltype(dim)::value;
-    if (rope->interleaved) launch_rope<T, D, true>(p, di->sms, s);
-    else launch_rope<T, D, false>(p, di->sms, s);
+    return rope->interleaved ? launch_rope<T, D, true>(p, di->sms, s) : launch_rope<T, D, false>(p, di->sms, s);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
-  if (dtype == ATTN_BF16) {
-    if (d == 64) go(__nv_bfloat16(), D64()); else go(__nv_bfloat16(), D128());
-  } else {
-    if (d == 64) go(0.f, D64()); else go(0.f, D128());
-  }
-  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  const cudaError_t e = dtype == ATTN_BF16 ? (d == 64 ? go(__nv_bfloat16(), D64()) : go(__nv_bfloat16(), D128()))
+                                           : (d == 64 ? go(0.f, D64()) : go(0.f, D128()));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attn_cache_write(const attn_cache_t* cache, const attn_batch_t* batch, const void* k,
@@ -324,17 +320,13 @@ int attn_cache_write(const attn_cache_t* cache, const attn_batch_t* batch, const
   auto go = [&](auto dim, auto eight) {
     constexpr int D = decltype(dim)::value;
     constexpr bool E = decltype(eight)::value;
-    if (inter) launch_cache_write<D, E, true>(p, di->sms, s);
-    else launch_cache_write<D, E, false>(p, di->sms, s);
+    return inter ? launch_cache_write<D, E, true>(p, di->sms, s) : launch_cache_write<D, E, false>(p, di->sms, s);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
-  if (cache->d == 64) {
-    if (e4m3) go(D64(), std::true_type()); else go(D64(), std::false_type());
-  } else {
-    if (e4m3) go(D128(), std::true_type()); else go(D128(), std::false_type());
-  }
-  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  const cudaError_t e = cache->d == 64 ? (e4m3 ? go(D64(), std::true_type()) : go(D64(), std::false_type()))
+                                       : (e4m3 ? go(D128(), std::true_type()) : go(D128(), std::false_type()));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* k_out, void* v_out, int N,
@@ -359,12 +351,11 @@ int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* 
   p.N = N;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == ATTN_E4M3;
-  if (cache->d == 64) {
-    if (e4m3) launch_cache_read<64, true>(p, batch->B, s); else launch_cache_read<64, false>(p, batch->B, s);
-  } else {
-    if (e4m3) launch_cache_read<128, true>(p, batch->B, s); else launch_cache_read<128, false>(p, batch->B, s);
-  }
-  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  const cudaError_t e =
+      cache->d == 64
+          ? (e4m3 ? launch_cache_read<64, true>(p, batch->B, s) : launch_cache_read<64, false>(p, batch->B, s))
+          : (e4m3 ? launch_cache_read<128, true>(p, batch->B, s) : launch_cache_read<128, false>(p, batch->B, s));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 size_t attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d) {
