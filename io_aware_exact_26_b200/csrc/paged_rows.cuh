@@ -5,10 +5,12 @@
 namespace attn {
 
 // ------------------------------------------------------------------ one query tile per CTA
-// Warps 0-7 softmax (two groups of 64 keys, thread = tile row = TMEM lane), warps
-// 8 and 10 producers of K (and Q) and of V, warp 9 MMA issuer and, for an e4m3 cache, warps
-// 11-18 that widen raw tiles to bf16 ones.  TMEM: S in two buffers, so S of the next tile is computed while the softmax
-// works on this one, and O.
+// Warps 0-15 softmax: four groups of 32 keys of each tile, thread = tile row = TMEM lane.
+// (Two groups of 64 keys: a tile took 3.9k cycles, chains of TMEM reads and exponentials that
+// two warps per scheduler cannot hide.)  Warps 16 and 18 producers of K (and Q) and of V,
+// warp 17 MMA issuer and, for an e4m3 cache, warps 19-26 that widen raw tiles to bf16 ones.
+// TMEM: S in two buffers, so S of the next tile is computed while the softmax works on this
+// one (P is written over S: keys [32k, 32k + 32) in columns [32k, 32k + 16)), and O.
 template <int D_, bool KV8_>
 struct RowsCfg {
   static constexpr int D = D_;
@@ -23,7 +25,7 @@ struct RowsCfg {
   static constexpr int kKTile = kTile;
   static constexpr int kQTile = kTile, kQBox = kBox;
   static constexpr int kWiden = KV8 ? 8 : 0;       // widening warps
-  static constexpr int kThreads = 352 + 32 * kWiden;
+  static constexpr int kThreads = 608 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;         // e4m3 codes of a tile
   // Raw stages, K and V tiles alternating.  An even number: the two producers run on their
   // own, so each needs its own stages (with 3, K could take one that V had yet to fill).
@@ -38,20 +40,20 @@ struct RowsCfg {
   static constexpr int kOffRaw = kOffV + KSK * kTile;
   static constexpr int kOffScale = kOffRaw + RST * kRawTile;  // 128 scale bytes per raw stage
   static constexpr int kOffSh = kOffScale + RST * 128;
-  static constexpr int kLayout = kOffSh + 5120;
+  static constexpr int kLayout = kOffSh + 8192;
   static constexpr int kSmem = kLayout + 1024;
   static_assert(kSmem <= 232448, "shared memory layout exceeds 227 KB");
 };
 
 struct RowsShared : PagedPipe {
-  float xmax[2][2][128];      // [parity of the quadrant's steps][group][row] partial row maxima
-  float xsum[2][128];
+  float xmax[2][4][128];      // [parity of the quadrant's steps][group][row] partial row maxima
+  float xsum[4][128];
   uint64_t p_ready[2];
-  uint64_t xbar[2][4];        // [parity][quadrant]: both groups' warps posted their maxima
+  uint64_t xbar[2][4];        // [parity][quadrant]: the four groups' warps posted their maxima
   uint64_t sbar[4];
   uint64_t o_free;
 };
-static_assert(sizeof(RowsShared) <= 5120, "RowsShared does not fit its slot");
+static_assert(sizeof(RowsShared) <= 8192, "RowsShared does not fit its slot");
 
 template <int D, bool KV8>
 __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
@@ -66,27 +68,27 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    paged_pipe_init<C>(sh, 10 + C::kWiden, 11 + C::kWiden);
+    paged_pipe_init<C>(sh, 18 + C::kWiden, 19 + C::kWiden);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.p_ready[i], 8);
-      for (int q = 0; q < 4; ++q) mbar_init(&sh.xbar[i][q], 2);
+      mbar_init(&sh.p_ready[i], 16);
+      for (int q = 0; q < 4; ++q) mbar_init(&sh.xbar[i][q], 4);
     }
-    for (int q = 0; q < 4; ++q) mbar_init(&sh.sbar[q], 2);
-    mbar_init(&sh.o_free, 8);
+    for (int q = 0; q < 4; ++q) mbar_init(&sh.sbar[q], 4);
+    mbar_init(&sh.o_free, 16);
     fence_barrier_init();
   }
   if (warp == 0) { tmem_alloc(&sh.tmem_base, C::kTmemCols); tmem_relinquish(); }
   grid_dependency_wait();
   grid_dependency_launch();
-  paged_plan(p, sh.plan, cta, warp == 8, lane);
+  paged_plan(p, sh.plan, cta, warp == 16, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
-  if (warp == 8) {
+  if (warp == 16) {
     paged_produce_k<C>(p, sh, &tmq, &tmk, m, cta, lane);
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------ MMA issuer
     // Per piece: S(0), S(1); then per step j: PV(j), S(j + 2) into the buffer PV(j) just
     // read (MMAs of one thread run in issue order, so PV(j) reads P(j) first).
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
           const uint32_t sbase = tmem + ((g & 1) ? C::kS1 : C::kS0);
 #pragma unroll
           for (int k2 = 0; k2 < 8; ++k2)
-            umma_ts_lo(tmem + C::kO, sbase + (k2 >> 2) * 64 + (k2 & 3) * 8, v_lo + ((k2 * 2048) >> 4), hi, idO,
+            umma_ts_lo(tmem + C::kO, sbase + (k2 >> 1) * 32 + (k2 & 1) * 8, v_lo + ((k2 * 2048) >> 4), hi, idO,
                        !(j == 0 && k2 == 0));
           umma_commit(&sh.v_done[vc & 7]);
         }
@@ -162,17 +164,17 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     paged_produce_v<C>(p, sh, &tmv, m, lane);
-  } else if (warp >= 11) {
-    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 352, lane, [](int, int) {});
+  } else if (warp >= 19) {
+    if constexpr (KV8) paged_widen<C>(sh, m, threadIdx.x - 608, lane, [](int, int) {});
   } else {
-    // ------------------------------------------------------------ softmax warps 0-7
-    const int grp = warp >> 2;                                  // keys [64 grp, 64 grp + 64)
+    // ------------------------------------------------------------ softmax warps 0-15
+    const int grp = warp >> 2;                                  // keys [32 grp, 32 grp + 32)
     const int quad = warp & 3;
     const int row = quad * 32 + lane;                           // tile row = TMEM lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    constexpr int OH = D / 2;
+    constexpr int OH = D / 4;
     const uint32_t o_base = lane_base + C::kO + grp * OH;
     const float c = p.cs;
     const uint64_t c2 = f2pack(c, c);
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       uint64_t lsum = f2pack(0.f, 0.f);
       for (int j = 0; j < w.n && ok; ++j) {
         const int g2 = gs + j, xp = xs & 1;
-        const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 64;
+        const uint32_t s_base = lane_base + ((g2 & 1) ? C::kS1 : C::kS0) + grp * 32;
         ok = __all_sync(0xffffffffu, tile_done_wait(sh.k_done, g2));
         if (!ok) break;
         if (!active) {
@@ -206,40 +208,32 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const int kbase = (w.j0 + j) * 128 + grp * 64;
+        const int kbase = (w.j0 + j) * 128 + grp * 32;
         const int lo = firstk - kbase, lim = lastk - kbase;        // visible columns [lo, lim]
-        const bool msk = __any_sync(0xffffffffu, valid && (lo > 0 || lim < 63));
+        const bool msk = __any_sync(0xffffffffu, valid && (lo > 0 || lim < 31));
+        uint32_t r[2][16];
+        tmem_ld16(s_base, r[0]);
+        tmem_ld16(s_base + 16, r[1]);
+        tmem_wait_ld();
+        reg_fence(r[0]);
+        reg_fence(r[1]);
+        if (msk) { mask16(r[0], 0, lo, lim); mask16(r[1], 16, lo, lim); }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        {
-          uint32_t r0[16], r1[16], r2[16], r3[16];
-          tmem_ld16(s_base, r0);
-          tmem_ld16(s_base + 16, r1);
-          tmem_ld16(s_base + 32, r2);
-          tmem_ld16(s_base + 48, r3);
-          tmem_wait_ld();
-          reg_fence(r0);
-          reg_fence(r1);
-          reg_fence(r2);
-          reg_fence(r3);
-          if (msk) { mask16(r0, 0, lo, lim); mask16(r1, 16, lo, lim); mask16(r2, 32, lo, lim); mask16(r3, 48, lo, lim); }
 #pragma unroll
-          for (int kk = 0; kk < 16; kk += 8) {
+        for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              mx4[e] = max3f(mx4[e], __uint_as_float(r0[kk + e]), __uint_as_float(r0[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r1[kk + e]), __uint_as_float(r1[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r2[kk + e]), __uint_as_float(r2[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r3[kk + e]), __uint_as_float(r3[kk + e + 4]));
-            }
-          }
-        }
+          for (int kk = 0; kk < 16; kk += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx4[e] = max3f(mx4[e], __uint_as_float(r[cc][kk + e]), __uint_as_float(r[cc][kk + e + 4]));
         sh.xmax[xp][grp][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.xbar[xp][quad]);
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[xp][quad], (xs >> 1) & 1));
         if (!ok) break;
         ++xs;
-        const float mx = fmaxf(sh.xmax[xp][0][row], sh.xmax[xp][1][row]);
+        const float mx = fmaxf(fmaxf(sh.xmax[xp][0][row], sh.xmax[xp][1][row]),
+                               fmaxf(sh.xmax[xp][2][row], sh.xmax[xp][3][row]));
         const float m_tile = mx == -INFINITY ? -INFINITY : mx * c;
         float alpha = 1.f;
         // a row that has seen no key keeps m_used = -inf (and p = 0) until it sees one
@@ -271,18 +265,14 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
         }
         const float mb = m_used == -INFINITY ? 0.f : m_used;
         const uint64_t nm2 = f2pack(-mb, -mb);
+        // the scores are still in registers; P goes over this group's own columns of S
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t r[16];
-          tmem_ld16(s_base + cc * 16, r);
-          tmem_wait_ld();
-          reg_fence(r);
-          if (msk) mask16(r, cc * 16, lo, lim);
+        for (int cc = 0; cc < 2; ++cc) {
           uint32_t pk[8];
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t xx =
-                ffma2(f2pack(__uint_as_float(r[2 * kk]), __uint_as_float(r[2 * kk + 1])), c2, nm2);
+                ffma2(f2pack(__uint_as_float(r[cc][2 * kk]), __uint_as_float(r[cc][2 * kk + 1])), c2, nm2);
             float x0, x1;
             f2unpack(xx, x0, x1);
             const float a0 = ex2_approx(x0), a1 = ex2_approx(x1);
@@ -297,7 +287,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&sh.p_ready[g2 & 1]);
       }
       if (!ok) break;
-      // epilogue: the two groups' sums, the last PV, O / l and the LSE of this piece
+      // epilogue: the four groups' sums, the last PV, O / l and the LSE of this piece
       const int glast = gs + w.n - 1;
       float l = 0.f;
       if (active) {
@@ -309,7 +299,7 @@ __global__ void __launch_bounds__(RowsCfg<D, KV8>::kThreads, 1)
       if (lane == 0) mbar_arrive(&sh.sbar[quad]);
       ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar[quad], uq & 1));
       if (!ok) break;
-      if (active) l = sh.xsum[0][row] + sh.xsum[1][row];
+      if (active) l = (sh.xsum[0][row] + sh.xsum[1][row]) + (sh.xsum[2][row] + sh.xsum[3][row]);
       ok = __all_sync(0xffffffffu, tile_done_wait(sh.v_done, glast));
       if (!ok) break;
       if (active) {
