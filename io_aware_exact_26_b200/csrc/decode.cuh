@@ -91,7 +91,7 @@ struct DecShared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2];        // S of step g complete in buffer g % 2
   uint64_t p_ready[2];       // P of step g written over buffer g % 2 by the 8 softmax warps
-  uint64_t pv_done;          // P V of a step complete
+  uint64_t pv_done[2];       // P V of step g complete, by g % 2: a waiter may be a step behind
   uint64_t xbar[2];          // [step parity]: both groups posted their maxima
   uint64_t sbar;             // both groups posted their sums
   uint64_t o_free;           // O read out by the epilogue
@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_ready[i], 8);
       mbar_init(&sh.xbar[i], 8);
+      mbar_init(&sh.pv_done[i], 1);
     }
-    mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.sbar, 8);
     mbar_init(&sh.o_free, 8);
     unit_ring_init(sh.ring, 9);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(320, 1)
           for (int k = 0; k < 8; ++k)
             umma_ts_lo(tmem + C::kO, sbase + (k >> 2) * 64 + (k & 3) * 8, v_lo + ((k * 2048) >> 4), hi, idO,
                        !(j == 0 && k == 0));
-          umma_commit(&sh.pv_done);
+          umma_commit(&sh.pv_done[g & 1]);
           umma_commit(&sh.v_empty[vst]);
         }
         __syncwarp();
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(320, 1)
         // S(j) was issued before PV(j - 1) (and after PV(j - 2), which its commit covers):
         // wait for PV(j - 1) before rescaling O
         if (__any_sync(0xffffffffu, need && j > 0)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, (g2 - 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[(g2 - 1) & 1], ((g2 - 1) >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -435,11 +435,10 @@ __global__ void __launch_bounds__(320, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&sh.sbar, uq & 1));
       if (!ok) break;
       const float l = sh.xsum[0][row] + sh.xsum[1][row];
-      // pv_done completes once per step.  S(glast) covered PV(glast - 2) only, so the
-      // phases of PV(glast - 1) and PV(glast) are waited for in turn (a parity wait
-      // can only tell apart the phase in progress and the one before it).
-      if (glast >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, (glast - 1) & 1));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done, glast & 1));
+      // PV(glast).  S(glast) covered PV(glast - 2), the one before it on this barrier, so the
+      // parity is unambiguous.  (One barrier for all steps, waited for at glast - 1 and glast in
+      // turn, would miss both if PV(glast) completed before a slow warp's first look.)
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[glast & 1], (glast >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
