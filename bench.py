@@ -2,6 +2,7 @@
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--impl ours|reference]
     python bench.py --sweep [--sweep-reps R] [--warmup W]
+    python bench.py --serve [--decode-workload NAME] [--sweep-reps R] [--warmup W]
 
 One step = one pass of the whole hot path over one batch: attn_fwd (O, LSE) then
 attn_bwd (dQ, dK, dV) for workloads that train, attn_fwd alone for forward-only
@@ -17,7 +18,8 @@ oracle instead (the reference arm), on a bounded sample of the same workload.
 ``--sweep`` times attn_fwd and attn_bwd separately over the sequence-length sweep
 (B*N and Hq*d fixed, N from 1K to 32K, d 64 and 128, causal and not) on one GPU
 and prints one JSON line per point: the median of R timed calls after W warm-up
-calls, each call's inputs larger than L2.
+calls, each call's inputs larger than L2.  ``--serve`` times decoding steps over a
+paged bf16 and e4m3 cache (rotate, write, attend).
 """
 from __future__ import annotations
 
@@ -440,6 +442,80 @@ def run_decode(args):
         torch.cuda.empty_cache()
 
 
+def run_serve(args):
+    """Decoding steps over a paged cache, timed apart: one JSON line per decode workload and
+    cache type.  A step is what a server does per token: attn_cache_write (rotate Q and K, put
+    K and V into the pages) and attn_paged.  Bound by HBM like run_decode."""
+    import torch
+    import io_aware_exact_26_b200 as attn
+
+    peaks, peaks_kind = load_peaks()
+    hbm = float(peaks["hbm_gbs"])
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    stream = torch.cuda.current_stream()
+    names = [args.decode_workload] if args.decode_workload else list(DECODE_WORKLOADS)
+    page = 64
+    for name in names:
+        w = DECODE_WORKLOADS[name]
+        T, per_seq = w.B * w.Nq, -(-w.Nk // page)
+        gen = torch.Generator(device=dev).manual_seed(w.Nk)
+        for kv in ("bf16", "e4m3"):
+            shape = (w.B * per_seq, w.Hkv, page, w.d)
+            dt = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+            row = w.d * 2 if kv == "bf16" else w.d + 1
+            cached = 2 * w.B * w.Nk * w.Hkv * row
+            copies = max(1, -(-2 * 126 * 2 ** 20 // cached))       # rotate past L2
+            caches = []
+            for _ in range(copies):
+                c = [torch.randn(shape, generator=gen, device=dev, dtype=torch.bfloat16).to(dt) for _ in range(2)]
+                c += [torch.full(shape[:3], 127, dtype=torch.uint8, device=dev) for _ in range(2)] if kv == "e4m3" else []
+                caches.append(c)
+            table = torch.randperm(shape[0], generator=gen, device=dev).to(torch.int32).reshape(w.B, per_seq)
+            cu = torch.arange(0, T + 1, w.Nq, dtype=torch.int32, device=dev)
+            kv_len = torch.full((w.B,), w.Nk, dtype=torch.int32, device=dev)
+            qkv = torch.randn((T, w.Hq + 2 * w.Hkv, w.d), generator=gen, device=dev, dtype=torch.bfloat16)
+            q, k, v = qkv[:, :w.Hq], qkv[:, w.Hq:w.Hq + w.Hkv], qkv[:, w.Hq + w.Hkv:]
+            freq, _ = attn.rope_inv_freq(w.d, device=dev)
+            q_out = torch.empty((T, w.Hq, w.d), dtype=torch.bfloat16, device=dev)
+            o, lse = torch.empty_like(q_out), torch.empty((T, w.Hq), dtype=torch.float32, device=dev)
+            ws = torch.empty(attn.attn_paged_workspace_size(T, w.B, w.Hq, w.Hkv, w.d), dtype=torch.uint8, device=dev)
+
+            def step(i):
+                c = caches[i % copies]
+                sc = dict(k_scale=c[2], v_scale=c[3]) if kv == "e4m3" else {}
+                attn.attn_cache_write(k, v, c[0], c[1], table, cu, kv_len, **sc, inv_freq=freq, q=q, q_out=q_out)
+                attn.attn_paged(q_out, c[0], c[1], table, cu, kv_len, **sc, o=o, lse=lse, scale=w.scale, workspace=ws)
+
+            for i in range(args.warmup):
+                step(i)
+            evs = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+                   for _ in range(args.sweep_reps)]
+            sampler = ClockSampler(0)
+            sampler.start()
+            for i, (a, b) in enumerate(evs):
+                a.record(stream)
+                step(i)
+                b.record(stream)
+            torch.cuda.synchronize()
+            clocks = sampler.stop()
+            if attn.attn_get_device_status() != 0:
+                raise SystemExit(f"device-side error in serve {name}")
+            ms = statistics.median(a.elapsed_time(b) for a, b in evs)
+            nbytes = acc.min_bytes_serve(T, w.Hq, w.Hkv, w.d, w.B * w.Nk, row)
+            gbs = nbytes / (ms * 1e-3) / 1e9
+            print(json.dumps({
+                "serve": name, "cache": kv, "page_size": page, "B": w.B, "Hq": w.Hq, "Hkv": w.Hkv, "new_tokens": w.Nq,
+                "cached": w.Nk, "d": w.d, "reps": args.sweep_reps, "warmup": args.warmup, "ms": round(ms, 4),
+                "roofline": {"bound": "hbm", "achieved": round(gbs, 1), "peak": hbm, "unit": "GB/s",
+                             "frac": round(gbs / hbm, 4), "algorithmic_bytes": nbytes,
+                             "peak_source": f"{peaks_kind} copy bandwidth"},
+                "l2": f"{copies} caches rotated ({cached / 1e6:.0f} MB each)", "gpu_launches_per_call": 3,
+                "clocks": clocks}), flush=True)
+            del caches, qkv, q, k, v, q_out, o, lse, ws
+            torch.cuda.empty_cache()
+
+
 def run_fp8(args):
     """FP8 forward (e4m3 inputs) next to the bf16 forward on the same shapes, timed apart.
     The fp8 roofline peak is the measured bf16 dense peak times the nominal fp8 : bf16
@@ -673,6 +749,8 @@ def main():
     ap.add_argument("--sweep", action="store_true", help="time the sequence-length sweep, one line per point")
     ap.add_argument("--sweep-reps", type=int, default=50)
     ap.add_argument("--decode", action="store_true", help="time split-KV decoding, one line per decode workload")
+    ap.add_argument("--serve", action="store_true",
+                    help="time decoding steps over a paged bf16 and e4m3 cache, two lines per decode workload")
     ap.add_argument("--fp8", action="store_true", help="time the fp8 forward next to the bf16 forward")
     ap.add_argument("--window", action="store_true", help="time local (sliding-window) attention, fwd and bwd")
     ap.add_argument("--ring", action="store_true",
@@ -688,6 +766,9 @@ def main():
         return
     if args.decode:
         run_decode(args)
+        return
+    if args.serve:
+        run_serve(args)
         return
     if args.fp8:
         run_fp8(args)

@@ -115,3 +115,11 @@ def flops_window(B, Hq, N, d, left, right, bwd=False):
     """4*d FLOPs per visible pair forward, 10*d backward (the dense counts restricted to
     the band; causal, (None, 0), gives exactly the halved-plus-diagonal count)."""
     return (10.0 if bwd else 4.0) * B * Hq * visible_pairs(N, left, right) * d
+
+
+def min_bytes_serve(T, Hq, Hkv, d, cached, cache_row):
+    """One serving step through the paged cache: the new tokens' Q, K and V read, Q rotated and
+    written, K and V put into the cache (cache_row bytes per row and head), then Q and the
+    ``cached`` positions of K and V read, O and LSE written."""
+    step = T * (2 * Hq + 2 * Hkv) * d * BF16 + 2 * T * Hkv * cache_row
+    return step + 2 * cached * Hkv * cache_row + 2 * T * Hq * d * BF16 + T * Hq * FP32

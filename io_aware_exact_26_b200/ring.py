@@ -77,6 +77,17 @@ def shard_chunks(rank: int, world: int, layout: str = "contiguous"):
     raise ValueError(f"layout must be one of {LAYOUTS}")
 
 
+def shard_positions(rank: int, world: int, N: int, layout: str = "contiguous"):
+    """Positions in the whole sequence of the N / world rows that ``rank`` holds, in local order
+    (int32): what ``attn_rope`` and ``attn_rope_bwd`` take to rotate a shard's q and k before the
+    ring and their gradients after it."""
+    chunks = shard_chunks(rank, world, layout)
+    n = N // (world * len(chunks))
+    if n * world * len(chunks) != N:
+        raise ValueError(f"N = {N} does not divide into {world * len(chunks)} chunks")
+    return torch.cat([torch.arange(c * n, (c + 1) * n, dtype=torch.int32) for c in chunks])
+
+
 def chunk_kind(a: int, b: int, causal: bool):
     """What query chunk a computes against key chunk b."""
     if not causal or b < a:

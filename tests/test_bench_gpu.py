@@ -61,3 +61,17 @@ def test_reference_arm_prints_the_same_metric():
     d = run_bench("--impl", "reference", "--steps", "1", "--warmup", "0")
     assert d["impl"] == "reference" and d["metric"] == "attention fwd+bwd TFLOPS" and d["unit"] == "TFLOPS"
     assert d["cpu_baseline"]["kind"] == "oracle" and d["e2e"]["h2d_bytes_per_step"] == 0
+
+
+def test_serve_prints_a_line_per_cache_type():
+    import bench
+    name = sorted(bench.DECODE_WORKLOADS)[-1]
+    out = subprocess.run([sys.executable, "bench.py", "--serve", "--decode-workload", name, "--sweep-reps", "5",
+                          "--warmup", "3"], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0, out.stderr[-2000:]
+    lines = [json.loads(ln) for ln in out.stdout.splitlines() if ln.startswith("{")]
+    assert [d["cache"] for d in lines] == ["bf16", "e4m3"] and all(d["serve"] == name for d in lines)
+    for d in lines:
+        r = d["roofline"]
+        assert d["ms"] > 0 and r["bound"] == "hbm" and 0 < r["frac"] < 1.2
+        assert abs(r["achieved"] - r["algorithmic_bytes"] / (d["ms"] * 1e-3) / 1e9) <= 0.01 * r["achieved"]

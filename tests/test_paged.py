@@ -195,3 +195,26 @@ def test_inv_freq_yarn_keeps_fast_pairs_and_slows_slow_ones():
 def test_inv_freq_refusals(kw):
     with pytest.raises(ValueError):
         attn.rope_inv_freq(device="cpu", **kw)
+
+
+# ------------------------------------------------------------------ positions of ring shards
+@pytest.mark.parametrize("layout", ["contiguous", "zigzag"])
+@pytest.mark.parametrize("world", [1, 2, 4])
+def test_shard_positions_rotate_a_shard_like_the_whole_sequence(layout, world):
+    from io_aware_exact_26_b200 import ring
+    from tests import paged_reference as ref
+    N, d = 48, 64
+    x = torch.randn(N, 2, d, generator=torch.Generator().manual_seed(1))
+    f = attn.rope_inv_freq(d, device="cpu")[0]
+    whole = ref.rotate(x, torch.arange(N), f, False)
+    seen = []
+    for rank in range(world):
+        pos = ring.shard_positions(rank, world, N, layout)
+        assert pos.dtype == torch.int32 and pos.shape == (N // world,)
+        assert torch.equal(ref.rotate(x[pos.long()], pos, f, False), whole[pos.long()])
+        n = N // (world * len(ring.shard_chunks(rank, world, layout)))
+        assert pos[::n].tolist() == [c * n for c in ring.shard_chunks(rank, world, layout)]
+        seen += pos.tolist()
+    assert sorted(seen) == list(range(N))
+    with pytest.raises(ValueError):
+        ring.shard_positions(0, 5, N, layout)
