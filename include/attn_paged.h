@@ -14,15 +14,17 @@
  * cache, the new ones included, so the new token in row t of sequence b has position
  *     pos = kv_len[b] - cu_q[b+1] + t.
  * A sequence may have no new token, or one (decoding), or many (a prompt's chunk), in
- * the same call.  Rows from cu_q[B] on (padding) are neither read nor written.
+ * the same call.  Rows before cu_q[0] and from cu_q[B] on (padding) are left alone.
  *
  * Pages.  The cache is a pool of num_pages pages of page_size positions (16, 32, 64, 128
  * or 256), shared by all sequences: position p of sequence b lies in row p % page_size of
  * page block_table[b * max_pages + p / page_size] (int32).  Only the table entries that
- * cover positions below kv_len[b] are read; the others may hold anything.  An entry
- * outside [0, num_pages), or a position beyond max_pages pages, is never followed: the
- * write of that token is skipped, reads see zeros there, and attn_get_device_status()
- * reports ATTN_ERR_DEVICE_PAGE once the work has run.
+ * cover positions below kv_len[b] (attn_paged: that some row sees) are followed; the others
+ * may hold anything.  An entry outside [0, num_pages), or a position beyond max_pages pages,
+ * is never followed: the write of that token is skipped, reads see zeros there, attention
+ * takes the sequence as max_pages pages long, and attn_get_device_status() reports
+ * ATTN_ERR_DEVICE_PAGE once the work has run.  kv_len is below 2^30; a negative one counts
+ * as 0.
  */
 #ifndef ATTN_B200_PAGED_H
 #define ATTN_B200_PAGED_H
@@ -133,7 +135,8 @@ int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* 
  * Both products run on the tensor cores with bf16 operands (e4m3 rows are widened on
  * chip, which is exact); sums and softmax statistics are fp32; P is rounded to bf16.
  * Masked scores never reach the sums, whatever the cache holds there; values of V at
- * positions below kv_len[b] have to be finite in the rows' visible 128-key tiles.
+ * positions below kv_len[b] have to be finite in the rows' visible 128-key tiles.  An
+ * infinite query value counts as NaN over an e4m3 cache.
  * The cache rows of this call's tokens must have been written before, on this stream or
  * ordered before it.
  * The keys are shared out evenly over the SMs by each CTA from cu_q and kv_len on the

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(256) attn_cache_write_kernel(const WriteParams
   int pos = 0;
   if (live) {
     pos = p.kv_len[b] - p.cu_q[b + 1] + t;
-    live = pos >= 0;
+    live = pos >= 0 && t >= p.cu_q[b];          // (rows before cu_q[0] belong to nobody)
   }
   const RopeUnit<T, D, INTER> unit(u, p.inv_freq ? p.rot : 0);
   const int h0 = blockIdx.y * p.heads_per_block;

@@ -90,7 +90,13 @@ struct PagedSeq {
     tok0 = p.cu_q[b];
     const int end = min(p.cu_q[b + 1], p.T);
     nq = tok0 >= 0 ? max(0, end - tok0) : 0;
+    // no further than the table leads: what lies behind is reported and not followed
+    const long long room = static_cast<long long>(p.max_pages) << p.c.page_shift;
     len = max(0, p.kv_len[b]);
+    if (len > room) {
+      record_bad_page();
+      len = static_cast<int>(room);
+    }
     // positions follow from the sequence's own count of tokens, also where T cuts it short
     pos0 = len - max(nq, p.cu_q[b + 1] - tok0);
     nblk = (nq + p.RI - 1) / p.RI;
@@ -282,11 +288,19 @@ struct PagedWalk {
     w.n = 0;
     w.slot = -1;
     if (left <= 0) return w;
-    while (i >= s.nblk) {                     // next head, next sequence that has tokens
+    if (i >= s.nblk) {                        // next head, or next sequence that has tokens
       i = 0;
-      if (++g >= p.Hkv || s.nblk == 0) {
+      if (++g >= p.Hkv) {
         g = 0;
-        if (++b >= p.B) { left = 0; return w; }
+        const int lane = threadIdx.x & 31;    // 32 sequences at a look: a padded batch may have many empty ones
+        unsigned some = 0;
+        for (++b; b < p.B; b += 32) {
+          const int c = b + lane;
+          some = __ballot_sync(0xffffffffu, c < p.B && min(p.cu_q[c + 1], p.T) > max(p.cu_q[c], 0));
+          if (some) break;
+        }
+        if (!some) { left = 0; return w; }
+        b += __ffs(some) - 1;
         s.load(p, b);
       }
     }

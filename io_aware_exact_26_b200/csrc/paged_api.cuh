@@ -334,7 +334,7 @@ int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* 
   int st = check_cache(cache);
   if (st == ATTN_OK) st = check_batch(batch, false);
   if (st != ATTN_OK) return st;
-  if (N < 0) return ATTN_ERR_INVALID_ARG;
+  if (N < 0 || N > (1 << 30)) return ATTN_ERR_INVALID_ARG;
   if (N == 0) return ATTN_OK;
   if (!k_out || !v_out) return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(batch->B) * cache->Hkv > 65535) return ATTN_ERR_INVALID_ARG;
@@ -409,7 +409,7 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   p.R = (form == 256 ? 128 : form) / G;
   p.RI = form == 256 ? 2 * p.R : p.R;
   p.causal = causal;
-  p.wl = window_left < 0 ? -1 : window_left;
+  p.wl = window_left < 0 ? -1 : window_left < (1 << 30) ? window_left : 1 << 30;
   p.cs = attn::folded_scale(scale);
   p.ctas = di->sms;
   p.slot_rows = W.slot_rows;

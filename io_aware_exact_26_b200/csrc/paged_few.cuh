@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
           }
         }
         const int k0 = (w.j0 + g - gs) * 128, key = k0 + row;
-        bool up = false;
+#pragma unroll
+        for (int q = 0; q < NR; ++q) x[q] *= c;
         if (!(k0 >= all_lo && k0 + 127 <= all_hi)) {
           int i = 0, h = 0;                                     // token and head of row q
 #pragma unroll
@@ -400,11 +401,9 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
             if (++h == p.G) { h = 0; ++i; }
           }
         }
+        bool up = false;
 #pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          x[q] *= c;
-          up |= x[q] > mu[q] + kRescaleTau;
-        }
+        for (int q = 0; q < NR; ++q) up |= x[q] > mu[q] + kRescaleTau;
         up = __any_sync(0xffffffffu, up);
         if (lane == 0) sh.vote[x2][par][wq] = up;
         ok = group_sync(&sh.vbar[x2][par], (g >> 2) & 1);

@@ -551,6 +551,77 @@ def test_bad_pages_are_reported_and_never_followed(attn):
     ok(attn)
 
 
+def test_lengths_beyond_the_table_are_reported_and_bounded(attn):
+    """A kv_len far past the table: the call ends at once, reports it, and leaves the other sequence's
+    result as it is alone."""
+    pool = Pool(1, 2, 16, 64, [30], False, seed=4)
+    (kc, vc, table), _ = pool.cuda()
+    q = normal((2, 4, 64), 5).cuda()
+    alone = attn.attn_paged(q[:1], kc, vc, table, ints([0, 1]).cuda(), ints([30]).cuda())
+    ok(attn)
+    both = table.repeat(2, 1).contiguous()
+    o, lse = attn.attn_paged(q, kc, vc, both, ints([0, 1, 2]).cuda(), ints([30, 1 << 29]).cuda())
+    assert attn.attn_get_device_status() == -10
+    assert torch.equal(o[0], alone[0][0]) and torch.equal(lse[0], alone[1][0])
+    ok(attn)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_sparse_batches_and_rows_that_belong_to_nobody(attn, e4m3):
+    """200 slots of which a few have tokens, packed rows that begin behind row 0: written, attended, and
+    every other row left alone."""
+    B, Hq, Hkv, d, page, first = 200, 4, 2, 64, 32, 3
+    new, lens = [0] * B, [0] * B
+    for b, n in ((0, 1), (37, 5), (38, 1), (120, 40), (199, 2)):
+        new[b], lens[b] = n, n + 90 + b
+    T = sum(new)
+    pool = Pool(B, Hkv, page, d, lens, e4m3, seed=2)
+    (kc, vc, table), scales = pool.cuda()
+    cu = bounds(new) + first
+    rows = normal((first + T + 2, Hq + 2 * Hkv, d), 6)
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    attn.attn_cache_write(k.cuda(), v.cuda(), kc, vc, table, cu.cuda(), ints(lens).cuda(), **scales)
+    o = torch.full((first + T + 2, Hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((first + T + 2, Hq), 3.0, device="cuda")
+    attn.attn_paged(q.cuda(), kc, vc, table, cu.cuda(), ints(lens).cuda(), **scales, o=o, lse=lse)
+    ok(attn)
+    outside = torch.ones(first + T + 2, dtype=torch.bool)
+    outside[first:first + T] = False
+    assert bool((o.cpu()[outside] == 3.0).all()) and bool((lse.cpu()[outside] == 3.0).all())
+    owned = torch.zeros(kc.shape[:3], dtype=torch.bool)
+    for b, L in enumerate(lens):
+        for p in range(L):
+            owned[int(table[b, p // page]), :, p % page] = True
+    if e4m3:
+        kv = [ref.widened(c.view(torch.uint8).cpu(), s.cpu()) for c, s in ((kc, scales["k_scale"]), (vc, scales["v_scale"]))]
+    else:
+        kv = [c.cpu().double() for c in (kc, vc)]
+    for c, n in zip(kv, "kv"):
+        stored = pool.value[n]
+        assert bool((c[~owned].isnan() == stored[~owned].isnan()).all())       # nothing written elsewhere
+    want = ref.attend(q[first:first + T], *kv, pool.table, bounds(new), lens, d ** -0.5)
+    check_attention((o[first:first + T], lse[first:first + T]), want)
+
+
+@pytest.mark.parametrize("T,Hq", [(1, 4), (1, 40), (30, 8), (200, 8)])
+def test_scale_zero_attends_uniformly_even_to_zero_rows(attn, T, Hq):
+    """scale = 0 over an e4m3 cache of zero rows under the smallest scale, and over a bf16 one."""
+    Hkv, page, d, L = 4, 16, 64, 333
+    for dt in (torch.float8_e4m3fn, torch.bfloat16):
+        kc = torch.zeros(21, Hkv, page, d, dtype=dt, device="cuda")
+        vc = torch.full((21, Hkv, page, d), 2.0, device="cuda").to(dt)
+        sc = dict(k_scale=torch.zeros(21, Hkv, page, dtype=torch.uint8, device="cuda"),
+                  v_scale=torch.full((21, Hkv, page), 127, dtype=torch.uint8, device="cuda")) if dt != torch.bfloat16 else {}
+        table = torch.arange(21, dtype=torch.int32).reshape(1, 21).cuda()
+        o, lse = attn.attn_paged(normal((T, Hq, d), 1).cuda(), kc, vc, table, bounds([T]).cuda(), ints([L]).cuda(), **sc,
+                                 scale=0.0, causal=False, window_left=(1 << 31) - 1)
+        ok(attn)
+        # Every score is 0 and every term of the sum 1.  Rows beyond one tile (bf16) take 2 of 8 pairs
+        # of terms at d = 64 from a cubic with a relative error of up to 7.5e-5 (its constant term is
+        # 7.2e-5 below 1), so the sum is off by at most 2/8 * 7.5e-5 = 1.9e-5, and its logarithm too.
+        assert bool((o == 2.0).all()) and float((lse - math.log(L)).abs().max()) <= 1e-5 + 2 / 8 * 7.5e-5
+
+
 def test_calls_on_two_streams_with_a_workspace_each(attn):
     """Two batches at once on two streams give what they give alone."""
     out = []
