@@ -33,9 +33,11 @@
 // its shared-memory traffic), so Q has to be 8-bit too, without losing anything: a bf16
 // value has 8 significant bits, e4m3 has 4, and q 2^-e = hi + lo with hi its nearest e4m3
 // and lo the rest.  With e from the row's largest magnitude (at most 448 2^e) the sum is
-// exact for values down to 2^-10 of it and off by at most 2^-18 of it below.  S = hi K +
-// lo K; the scales 2^e of a query row and of a key multiply the scores in the softmax
-// threads (a thread has one key).  V is widened to bf16, as its products with P need.
+// exact for values down to 2^-10 of it and off by at most 2^-18 of it below.  hi and lo are
+// columns of the same product (the MMA thread, which issues 8 small instructions per P V,
+// bounds an e4m3 tile, so S should take few), and the softmax thread adds the two; the scales
+// 2^e of a query row and of its key multiply the sum.  V is widened to bf16, as its products
+// with P need.
 #pragma once
 #include "paged.cuh"
 
@@ -55,7 +57,9 @@ struct FewCfg {
   static constexpr int kQTile = NB * kQBox;
   static constexpr int kPTile = 2 * kQBox;         // P^T: NQ rows of 128 keys
   static constexpr int QST = (NQ == 32 && D == 128 && !KV8) ? 1 : 2;
-  static constexpr int kQ8 = K8 ? 2 * kQBox : 0;   // hi and lo parts of Q, 128-byte rows
+  static constexpr int NH = NR < 8 ? 8 : NR;       // K8: rows 0 .. NR - 1 hi parts of Q, from NH on lo parts
+  static constexpr int NS = K8 ? 2 * NH : NQ;      // columns of S^T
+  static constexpr int kQ8 = K8 ? NS * 128 : 0;    // both parts, 128-byte rows
   static constexpr int KSK = K8 ? (NQ == 32 && D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
   static constexpr int KSV = KV8 ? (D == 128 ? 2 : 3) : KSK;
   // S(g) completes behind PV(g - SA), so P(g) may take the buffer of P(g - NP) for NP >= SA
@@ -73,8 +77,9 @@ struct FewCfg {
   static constexpr int kRawFit = kRoom / (kRawTile + 128);
   static constexpr int RST = KV8 ? (kRawFit < 8 ? kRawFit : 8) : 0;   // as many raw stages as fit: bytes in flight
   static constexpr int kRawMod = KV8 ? RST : 1;
-  static constexpr int kO = 4 * NQ;                // TMEM: S buffers at 0, NQ, 2 NQ, 3 NQ, then O of each group
-  static constexpr int kTmemCols = NQ == 16 ? 128 : 256;
+  static constexpr int kO = 4 * NS;                // TMEM: S buffers at 0, NS, 2 NS, 3 NS, then O of each group
+  static constexpr int kTmemUsed = kO + 2 * NQ;
+  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = KSK * kKTile;
   static constexpr int kOffRaw = kOffV + KSV * kTile;
@@ -217,7 +222,7 @@ __device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float
     }
     const int off = r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
     *reinterpret_cast<uint2*>(q8 + off) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(q8 + C::kQBox + off) = make_uint2(lo[0], lo[1]);
+    *reinterpret_cast<uint2*>(q8 + C::NH * 128 + off) = make_uint2(lo[0], lo[1]);
     if (c == 0) cq[r] = e8m0_value(static_cast<uint32_t>(e + 127));
   }
 }
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------ MMA issuer (one thread)
     const bool leader = elect_one();
-    constexpr uint32_t idS = KV8 ? idesc_e4m3_f32(128, NQ, false, false) : idesc_bf16_f32(128, NQ, false, false);
+    constexpr uint32_t idS = KV8 ? idesc_e4m3_f32(128, C::NS, false, false) : idesc_bf16_f32(128, NQ, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(128, NQ, true, false);
     constexpr uint32_t hi = sdesc_hi_sw128(1024);
     const uint32_t q_lo0 = sdesc_lo(smem_u32(KV8 ? sQ8 : m.q), 16);
@@ -291,14 +296,11 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
           const int st = g % C::KSK;
           if (!mbar_wait(&sh.k_full[st], (g / C::KSK) & 1)) return false;
           tc_fence_after();
-          const uint32_t k_lo = k_lo0 + st * (C::kKTile >> 4), d = tmem + (g & 3) * NQ;
+          const uint32_t k_lo = k_lo0 + st * (C::kKTile >> 4), d = tmem + (g & 3) * C::NS;
           if constexpr (KV8) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int k2 = 0; k2 < D / 32; ++k2)
-                umma_ss_f8_lo(d, k_lo + ((k2 * 32) >> 4), q_lo + ((part * C::kQBox + k2 * 32) >> 4), hi, idS,
-                              part + k2 > 0);
+            for (int k2 = 0; k2 < D / 32; ++k2)
+              umma_ss_f8_lo(d, k_lo + ((k2 * 32) >> 4), q_lo + ((k2 * 32) >> 4), hi, idS, k2 > 0);
           } else {
 #pragma unroll
             for (int k2 = 0; k2 < D / 16; ++k2)
@@ -378,10 +380,15 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float x[NR];
-        few_tmem_ld<NR>(lane_base + (g & 3) * NQ, x);
+        few_tmem_ld<NR>(lane_base + (g & 3) * C::NS, x);
         float c = p.cs;
         if constexpr (KV8) {
-          c *= e8m0_value(m.kscale[(g & 7) * 128 + row]);       // this key's scale
+          float lo[NR];
+          few_tmem_ld<NR>(lane_base + (g & 3) * C::NS + C::NH, lo);
+#pragma unroll
+          for (int q = 0; q < NR; ++q) x[q] += lo[q];
+          // this key's scale; the floor (below any that matters) keeps -inf times c at -inf
+          c = fmaxf(c * e8m0_value(m.kscale[(g & 7) * 128 + row]), 1e-37f);
 #pragma unroll
           for (int q = 0; q < NR; q += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&sh.cq[uq & 3][q]);
@@ -389,8 +396,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
           }
         }
         const int k0 = (w.j0 + g - gs) * 128, key = k0 + row;
-#pragma unroll
-        for (int q = 0; q < NR; ++q) x[q] *= c;
+        bool up = false;
         if (!(k0 >= all_lo && k0 + 127 <= all_hi)) {
           int i = 0, h = 0;                                     // token and head of row q
 #pragma unroll
@@ -401,9 +407,11 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
             if (++h == p.G) { h = 0; ++i; }
           }
         }
-        bool up = false;
 #pragma unroll
-        for (int q = 0; q < NR; ++q) up |= x[q] > mu[q] + kRescaleTau;
+        for (int q = 0; q < NR; ++q) {
+          x[q] *= c;
+          up |= x[q] > mu[q] + kRescaleTau;
+        }
         up = __any_sync(0xffffffffu, up);
         if (lane == 0) sh.vote[x2][par][wq] = up;
         ok = group_sync(&sh.vbar[x2][par], (g >> 2) & 1);
