@@ -15,7 +15,9 @@
 // from cu_q and kv_len alone (no plan from the host, no counter), so a captured launch
 // follows the lengths.  A CTA's share cuts at most two items; a cut item's parts go to
 // the workspace (two slots per CTA, independent of lengths) and the merge kernel joins
-// them in key order, so results do not depend on timing.
+// them in key order, so results do not depend on timing.  Items of few tiles are not cut but
+// go to the CTA in whose share they begin, where writing and merging parts of many rows
+// would cost more than the imbalance (p.whole).
 #pragma once
 #include "cache.cuh"
 #include "fwd.cuh"
@@ -33,6 +35,7 @@ struct PagedParams {
   int Hq, Hkv, G, R;          // R tokens per tile, G * R <= 128
   int RI;                     // tokens per item: R * teams
   int causal, wl;             // wl < 0: no window
+  int whole;                  // items of up to this many tiles are not cut (see PagedPlan)
   float cs;                   // scale * log2(e), floored (folded_scale)
   int ctas;                   // CTAs of the launch
   int slot_rows;              // rows of a workspace slot
@@ -135,6 +138,7 @@ struct PagedPlan {
   long long rest;             // begin, counted from the first tile of sequence b
   long long head_tiles;       // tiles of one (b, g)
   int parts;                  // C: CTAs that have a share
+  int whole;                  // p.whole, but 4 at most where a share is under 2 tiles: there CTAs are left over
   int b;
 };
 
@@ -180,6 +184,7 @@ __device__ __forceinline__ void paged_plan_warp(const PagedParams& p, PagedPlan&
   if (lane == 0) {
     pl.total = total;
     pl.parts = parts;
+    pl.whole = total < 2LL * p.ctas ? min(p.whole, 4) : p.whole;
     pl.begin = begin;
     pl.end = end;
     pl.b = p.B;
@@ -227,6 +232,7 @@ __device__ __forceinline__ void paged_plan_block(const PagedParams& p, PagedPlan
   if (threadIdx.x == 0) {
     pl.total = total;
     pl.parts = parts;
+    pl.whole = total < 2LL * p.ctas ? min(p.whole, 4) : p.whole;
     pl.begin = begin;
     pl.end = end;
   }
@@ -287,40 +293,48 @@ struct PagedWalk {
     PagedSeg w;
     w.n = 0;
     w.slot = -1;
-    if (left <= 0) return w;
-    if (i >= s.nblk) {                        // next head, or next sequence that has tokens
-      i = 0;
-      if (++g >= p.Hkv) {
-        g = 0;
-        const int lane = threadIdx.x & 31;    // 32 sequences at a look: a padded batch may have many empty ones
-        unsigned some = 0;
-        for (++b; b < p.B; b += 32) {
-          const int c = b + lane;
-          some = __ballot_sync(0xffffffffu, c < p.B && min(p.cu_q[c + 1], p.T) > max(p.cu_q[c], 0));
-          if (some) break;
+    while (left > 0) {
+      if (i >= s.nblk) {                      // next head, or next sequence that has tokens
+        i = 0;
+        if (++g >= p.Hkv) {
+          g = 0;
+          const int lane = threadIdx.x & 31;  // 32 sequences at a look: a padded batch may have many empty ones
+          unsigned some = 0;
+          for (++b; b < p.B; b += 32) {
+            const int c = b + lane;
+            some = __ballot_sync(0xffffffffu, c < p.B && min(p.cu_q[c + 1], p.T) > max(p.cu_q[c], 0));
+            if (some) break;
+          }
+          if (!some) { left = 0; return w; }
+          b += __ffs(some) - 1;
+          s.load(p, b);
         }
-        if (!some) { left = 0; return w; }
-        b += __ffs(some) - 1;
-        s.load(p, b);
       }
+      int n;
+      s.range(p, i, w.kmin, w.j0, n);
+      if (n <= pl.whole && skip > 0) {         // begun in the share before: all of it went there
+        left -= n - skip;
+        skip = 0;
+        ++i;
+        continue;
+      }
+      w.b = b;
+      w.g = g;
+      w.tok0 = s.tok0 + i * p.RI;
+      w.ntok = min(p.RI, s.nq - i * p.RI);
+      w.pos0 = s.pos0 + i * p.RI;
+      w.len = s.len;
+      w.j0 += skip;
+      const int have = n - skip;
+      w.n = n <= pl.whole || left >= have ? have : static_cast<int>(left);
+      if (skip > 0) w.slot = 2 * cta;
+      else if (w.n < n) w.slot = 2 * cta + 1;
+      if (skip == 0 && w.n < n) cut_end = pl.end - left + n;   // the first part of a cut item
+      left -= w.n;
+      skip = 0;
+      ++i;
+      return w;
     }
-    int n;
-    s.range(p, i, w.kmin, w.j0, n);
-    w.b = b;
-    w.g = g;
-    w.tok0 = s.tok0 + i * p.RI;
-    w.ntok = min(p.RI, s.nq - i * p.RI);
-    w.pos0 = s.pos0 + i * p.RI;
-    w.len = s.len;
-    w.j0 += skip;
-    const int have = n - skip;
-    w.n = static_cast<int>(left < have ? left : have);
-    if (skip > 0) w.slot = 2 * cta;
-    else if (w.n < n) w.slot = 2 * cta + 1;
-    if (skip == 0 && w.n < n) cut_end = pl.end - left + n;   // the first part of a cut item
-    left -= w.n;
-    skip = 0;
-    ++i;
     return w;
   }
 };
