@@ -705,8 +705,9 @@ __device__ __forceinline__ void paged_widen(PagedPipe& sh, const PagedSmem& m, i
           *reinterpret_cast<uint4*>(row + ((cc ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
         };
-        // Passes whose loads are in flight together.  Few: the loops of a kernel's five kinds of warps
-        // share the instruction caches (4 passes: 182-201 us, 2: 170-184, 64 x 8K at d = 128).
+        // Passes whose loads are in flight together.  Few: shorter loops measured
+        // faster (4 passes: 182-201 us, 2: 170-184, 64 x 8K at d = 128); why was not isolated (missing
+        // instructions are 0.9 of the 8.8 cycles between a warp's issues now).
         constexpr int NB = NP < 2 ? NP : 2;
 #pragma unroll 1
         for (int i0 = 0; i0 < NP; i0 += NB) {

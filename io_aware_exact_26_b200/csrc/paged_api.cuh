@@ -410,7 +410,7 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   p.causal = causal;
   p.wl = window_left < 0 ? -1 : window_left < (1 << 30) ? window_left : 1 << 30;
   // A part of a few rows costs little; parts of a whole tile's rows are worth it from 13 key
-  // tiles on (a 1000-token prompt: 51 us with every item cut where the shares meet, 32 so).
+  // tiles on (a 1000-token prompt: 51 us with every item cut where the shares meet, 33 so).
   p.whole = form <= 32 ? 0 : 12;
   p.cs = attn::folded_scale(scale);
   p.ctas = di->sms;
