@@ -155,12 +155,25 @@ bool make_q_map(CUtensorMap* m, const void* q, const attn_strides_t* st, int T, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows up to which the kernel for few rows is taken.  Its softmax grows with the rows, that
+// of the 128-row kernel does not; but the latter takes longer per tile than a tile's bytes
+// where those are few (d = 64), and longer still where it has to widen K (e4m3).  Few rows
+// against the 128-row kernel, us, 16 sequences of 8K at 4 heads to 8, and 32 of 512:
+//   bf16, d = 128:  8 rows 77 : 73, 24 : 21;  32 rows 143 : 75, 71 : 25;  4 rows 20 : 25 at 32 of 512
+//   bf16, d = 64:   8 rows 52 : 64, 24 : 20;  16 rows 69 : 64, 35 : 22
+//   e4m3, d = 64:   8 rows 57 : 78, 32 : 25;  16 rows 93 : 77, 51 : 28
+//   e4m3, d = 128:  16 rows 87 : 119, 47 : 34;  32 rows 147 : 121, 79 : 37
+// The other side is the faster one past these limits on long caches of one query head to
+// a cache head (d = 64, 16 tokens on 65K: bf16 176 : 238; e4m3, d = 128, 32 tokens: 338 : 455).
+constexpr int few_rows_limit(int d, bool kv8) { return d == 64 ? 8 : kv8 ? 16 : 4; }
+
 // Query rows per item, by the batch's mean: the smallest build of the kernel for few rows
 // that takes a sequence's rows, else 128, or 256 (two tiles, bf16 cache) where a sequence has
 // more than one tile's.  Any form is right for any lengths.
-int paged_form(int T, int B, int G, int dtype) {
+int paged_form(int T, int B, int G, int d, int dtype) {
   const long long rows = static_cast<long long>(G) * ((T + B - 1) / B);
-  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || dtype == ATTN_E4M3 ? 128 : 256;
+  if (rows <= few_rows_limit(d, dtype == ATTN_E4M3)) return rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+  return rows <= 128 || dtype == ATTN_E4M3 ? 128 : 256;
 }
 
 // Workspace of the cut items: descriptors, LSE of the parts, then their O (fp32).
@@ -213,12 +226,13 @@ template <int D, bool KV8>
 int launch_paged_form(int form, const void* q, const attn_strides_t* q_strides, const attn_cache_t* cache,
                       const attn::PagedParams& p, cudaStream_t s) {
 #define ATTN_FEW(NR) \
-  if (form == NR) \
-    return launch_paged<attn::FewCfg<D, KV8, NR>>(attn::attn_paged_few_kernel<D, KV8, NR>, q, q_strides, cache, p, s);
+  if constexpr (NR <= few_rows_limit(D, KV8)) { \
+    if (form == NR) \
+      return launch_paged<attn::FewCfg<D, KV8, NR>>(attn::attn_paged_few_kernel<D, KV8, NR>, q, q_strides, cache, p, s); \
+  }
   ATTN_FEW(4)
   ATTN_FEW(8)
   ATTN_FEW(16)
-  ATTN_FEW(32)
 #undef ATTN_FEW
   if constexpr (!KV8) {
     if (form == 256)
@@ -363,8 +377,8 @@ size_t attn_paged_workspace_size(int T, int B, int Hq, int Hkv, int d) {
   if (device_info(&di) != 0) return 0;
   // enough for either cache type
   const int G = Hq / Hkv;
-  const size_t a = paged_ws(T, G, paged_form(T, B, G, ATTN_BF16), d, di->sms).total;
-  const size_t b = paged_ws(T, G, paged_form(T, B, G, ATTN_E4M3), d, di->sms).total;
+  const size_t a = paged_ws(T, G, paged_form(T, B, G, d, ATTN_BF16), d, di->sms).total;
+  const size_t b = paged_ws(T, G, paged_form(T, B, G, d, ATTN_E4M3), d, di->sms).total;
   return a > b ? a : b;
 }
 
@@ -383,7 +397,7 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   DeviceInfo* di = nullptr;
   if (device_info(&di) != 0) return ATTN_ERR_UNSUPPORTED;
   const int d = cache->d, G = Hq / cache->Hkv;
-  const int form = paged_form(batch->T, batch->B, G, cache->dtype);
+  const int form = paged_form(batch->T, batch->B, G, d, cache->dtype);
   const PagedWs W = paged_ws(batch->T, G, form, d, di->sms);
   if (workspace && workspace_bytes < W.total) return ATTN_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -411,7 +425,7 @@ int attn_paged(const void* q, const attn_strides_t* q_strides, const attn_cache_
   p.wl = window_left < 0 ? -1 : window_left < (1 << 30) ? window_left : 1 << 30;
   // A part of a few rows costs little; parts of a whole tile's rows are worth it from 13 key
   // tiles on (a 1000-token prompt: 51 us with every item cut where the shares meet, 33 so).
-  p.whole = form <= 32 ? 0 : 12;
+  p.whole = form <= 16 ? 0 : 12;
   p.cs = attn::folded_scale(scale);
   p.ctas = di->sms;
   p.slot_rows = W.slot_rows;

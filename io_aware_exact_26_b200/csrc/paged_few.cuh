@@ -7,9 +7,9 @@
 // of the tensor-core tile and the query rows its NQ columns,
 //     S^T = K Q^T   [128 keys x NQ],      O^T += V^T P^T   [d x NQ],
 // and a softmax thread owns a key, with the scores of NR rows: the kernel is built for NR = 4,
-// 8, 16 and 32 rows per item (NQ = 16 is the least the tensor cores take), because a thread's
-// registers and the code's size follow NR (16 rows' code for 4 rows spent most of its time
-// on instruction fetches).  What crosses lanes is the maximum over keys, and softmax
+// 8 and 16 rows per item (NQ = 16 is the least the tensor cores take), because a thread's
+// work, registers and code follow NR (one build for all: 410 us, 64 x 8K over e4m3, pages
+// of 16; a build per row count: 395).  From there on the 128-row kernel is faster.  What crosses lanes is the maximum over keys, and softmax
 // needs no exact one: the exponent base of a row may be any number as long as O and the
 // sum use the same.  A tile's threads vote whether any score passes its row's base by
 // 2^kRescaleTau; only then (the first tiles of an item) are the maxima reduced, the base
@@ -46,7 +46,8 @@ namespace attn {
 template <int D_, bool KV8_, int NR_>
 struct FewCfg {
   static constexpr int D = D_, NR = NR_;
-  static constexpr int NQ = NR < 16 ? 16 : NR;     // columns of S^T and O^T
+  static constexpr int NQ = 16;                    // columns of S^T and O^T
+  static_assert(NR == 4 || NR == 8 || NR == 16, "rows per item");
   static constexpr bool KV8 = KV8_, K8 = KV8_;
   static constexpr int kTile = 128 * D * 2;        // bf16 tile
   static constexpr int kTeams = 1;
@@ -56,22 +57,22 @@ struct FewCfg {
   static constexpr int kQBox = NQ * 128;
   static constexpr int kQTile = NB * kQBox;
   static constexpr int kPTile = 2 * kQBox;         // P^T: NQ rows of 128 keys
-  static constexpr int QST = (NQ == 32 && D == 128 && !KV8) ? 1 : 2;
+  static constexpr int QST = 2;
   static constexpr int NH = NR < 8 ? 8 : NR;       // K8: rows 0 .. NR - 1 hi parts of Q, from NH on lo parts
   static constexpr int NS = K8 ? 2 * NH : NQ;      // columns of S^T
   static constexpr int kQ8 = K8 ? NS * 128 : 0;    // both parts, 128-byte rows
-  static constexpr int KSK = K8 ? (NQ == 32 && D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
+  static constexpr int KSK = K8 ? 4 : D == 128 ? 3 : 6;
   static constexpr int KSV = KV8 ? (D == 128 ? 2 : 3) : KSK;
   // S(g) completes behind PV(g - SA), so P(g) may take the buffer of P(g - NP) for NP >= SA
-  static constexpr int SA = NQ == 16 ? 3 : 2;
-  static constexpr int NP = NQ == 16 ? 4 : 2;
+  static constexpr int SA = 3;
+  static constexpr int NP = 4;
   // K8: the scale bytes of the last 8 K tiles are kept: a tile is filled in KSK tiles ahead of
   // S, S runs SA ahead of the softmax
   static_assert(SA <= KSK && SA <= KSV + 1 && NP >= SA && KSK <= 8 && KSV <= 8 && (!K8 || KSK + SA + 1 <= 8), "stages");
-  static constexpr int kWiden = KV8 ? (NQ == 16 ? 8 : 4) : 0;
+  static constexpr int kWiden = KV8 ? 8 : 0;
   static constexpr int kThreads = 352 + 32 * kWiden;
   static constexpr int kRawTile = 128 * D;
-  static constexpr int kShared = NQ == 16 ? 4096 : 6144;
+  static constexpr int kShared = 4096;
   static constexpr int kRoom = 232448 - 1024 - KSK * kKTile - KSV * kTile - QST * (kQTile + kQ8) - NP * kPTile -
                                1024 - kShared;
   static constexpr int kRawFit = kRoom / (kRawTile + 128);
@@ -160,8 +161,7 @@ __device__ __forceinline__ void few_tmem_ld(uint32_t addr, float (&f)[NR]) {
   uint32_t r[NR];
   if constexpr (NR == 4) tmem_ld4(addr, r);
   else if constexpr (NR == 8) tmem_ld8(addr, r);
-  else if constexpr (NR == 16) tmem_ld16(addr, r);
-  else tmem_ld32(addr, r);
+  else tmem_ld16(addr, r);
   tmem_wait_ld();
   reg_fence(r);
 #pragma unroll
@@ -169,16 +169,12 @@ __device__ __forceinline__ void few_tmem_ld(uint32_t addr, float (&f)[NR]) {
 }
 template <int NR>
 __device__ __forceinline__ void few_tmem_st(uint32_t addr, const float (&f)[NR]) {
-  constexpr int N = NR < 16 ? NR : 16;
+  uint32_t r[NR];
 #pragma unroll
-  for (int b = 0; b < NR; b += N) {
-    uint32_t r[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[b + i]);
-    if constexpr (N == 4) tmem_st4(addr + b, r);
-    else if constexpr (N == 8) tmem_st8(addr + b, r);
-    else tmem_st16(addr + b, r);
-  }
+  for (int i = 0; i < NR; ++i) r[i] = __float_as_uint(f[i]);
+  if constexpr (NR == 4) tmem_st4(addr, r);
+  else if constexpr (NR == 8) tmem_st8(addr, r);
+  else tmem_st16(addr, r);
 }
 
 // 2^(byte - 127), also for byte 0 (subnormal).

@@ -419,6 +419,17 @@ def test_paged_attention_of_ragged_chunks(attn, Hq, Hkv, d, page, e4m3, window):
     check_attention(*run_paged(attn, (Hq, Hkv, d, page, e4m3, new, lens, True, window), seed=d))
 
 
+@pytest.mark.parametrize("rows", [3, 4, 5, 8, 9, 16, 17, 32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_paged_attention_around_each_row_count_of_a_kernel(attn, rows, d, e4m3):
+    """The mean of rows per sequence picks the kernel: just at, below and above each step, with a
+    sequence of many times the mean in it, one of no token, and one query head to a cache head."""
+    new, lens = [rows, 0, 4 * rows - 2, 1, 1], [300, 40, 190, 129, 1]
+    new[0] = 5 * rows - sum(new[1:])                                  # mean of exactly `rows`
+    check_attention(*run_paged(attn, (2, 2, d, 32, e4m3, new, lens, True, None), seed=rows * d))
+
+
 @pytest.mark.parametrize("Hq", [4, 8, 12, 32, 64])
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_paged_attention_is_repeatable(attn, Hq, e4m3):
