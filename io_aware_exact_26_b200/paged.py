@@ -5,7 +5,10 @@ Argument marshalling only, as in ``binding``.  Tensors may be views as long as t
 dimension is contiguous (slices of a fused projection, a cache interleaved page by page);
 the others' strides are passed on.  All tensors of a call are on one CUDA device, which
 need not be the current one; the work goes to that device's current stream unless
-``stream`` is given.
+``stream`` is given.  Outputs that a call allocates belong to the stream that it works on:
+memory that another stream may still be using is not taken for them, and a fill that they
+need is ordered before the kernel.  A caller who hands ``stream`` orders the inputs' producers
+and the outputs' users against it, as for any work on a second stream.
 """
 from __future__ import annotations
 
@@ -69,6 +72,15 @@ def _stream(stream, index):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(index)       # torch.cuda.current_stream, without the object
+
+
+def _new(like, shape, dtype, stream, zero=False):
+    """An output on like's device, in memory of the call's stream and, with zero, filled on it."""
+    make = like.new_zeros if zero else like.new_empty
+    if stream is None:
+        return make(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype)
 
 
 def _tensor(t, name, dtype, index=None, dim=None, contiguous=False):
@@ -175,7 +187,7 @@ def _rope_call(name, inverse, q, k, positions, inv_freq, interleaved, mscale, q_
         if k.shape != ((B, Hkv, N, d) if len(sh) == 4 else (N, Hkv, d)):
             raise ValueError("k must have q's shape apart from the number of heads")
         if k_out is None:
-            k_out = k.new_empty(k.shape)
+            k_out = _new(k, k.shape, dt, stream)
         else:
             _check_out(k_out, k, "k_out", dev)
         kp, kop, ks, kos = k.data_ptr(), k_out.data_ptr(), _strides(k), _strides(k_out)
@@ -187,7 +199,7 @@ def _rope_call(name, inverse, q, k, positions, inv_freq, interleaved, mscale, q_
         raise ValueError("positions must have one entry per token: [N], or [B, N] for dense tensors")
     rope = _rope_struct(inv_freq, interleaved, mscale, dev)
     if q_out is None:
-        q_out = q.new_empty(sh)
+        q_out = _new(q, sh, dt, stream)
     else:
         _check_out(q_out, q, "q_out", dev)
     with _on(dev):
@@ -296,7 +308,7 @@ def attn_cache_write(k, v, k_cache, v_cache, block_table, cu_q, kv_len, *, k_sca
         if q.shape != (T, Hq, d):
             raise ValueError("q must be [T, Hq, d]")
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = _new(q, q.shape, _bf16, stream)
         else:
             _check_out(q_out, q, "q_out", dev)
         qp, qop, qs, qos = q.data_ptr(), q_out.data_ptr(), _strides(q), _strides(q_out)
@@ -326,9 +338,9 @@ def attn_cache_read(k_cache, v_cache, block_table, kv_len, *, k_scale=None, v_sc
         N = k_out.shape[2]
     shape = (batch.B, Hkv, int(N), d)
     if k_out is None:
-        k_out = kv_len.new_zeros(shape, dtype=_bf16)
+        k_out = _new(kv_len, shape, _bf16, stream, zero=True)
     if v_out is None:
-        v_out = kv_len.new_zeros(shape, dtype=_bf16)
+        v_out = _new(kv_len, shape, _bf16, stream, zero=True)
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         _tensor(t, n, _bf16, dev, 4, contiguous=True)
         if t.shape != shape:
@@ -363,13 +375,13 @@ def attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *, k_scale=None, 
         raise ValueError("q and the cache differ in head size")
     batch = _batch_struct(block_table, cu_q, kv_len, T, dev)
     if o is None:
-        o = q.new_empty((T, Hq, d))
+        o = _new(q, (T, Hq, d), _bf16, stream)
     else:
         _tensor(o, "o", _bf16, dev, 3, contiguous=True)
         if o.shape != (T, Hq, d):
             raise ValueError("o must be [T, Hq, d]")
     if lse is None:
-        lse = q.new_empty((T, Hq), dtype=_f32)
+        lse = _new(q, (T, Hq), _f32, stream)
     else:
         _tensor(lse, "lse", _f32, dev, 2, contiguous=True)
         if lse.shape != (T, Hq):
