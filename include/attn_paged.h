@@ -133,7 +133,10 @@ int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* 
  *   lse : fp32 [T][Hq], contiguous.  Hq is a multiple of Hkv with Hq / Hkv <= 128; query
  *   head h reads KV head h / (Hq / Hkv).
  * Both products run on the tensor cores with bf16 operands (e4m3 rows are widened on
- * chip, which is exact); sums and softmax statistics are fp32; P is rounded to bf16.
+ * chip, which is exact), but for few query rows over an e4m3 cache: there K is multiplied
+ * as it lies, by Q in four e4m3 parts, which hold a query value exactly down to 2^-35 of
+ * its row's largest magnitude and to 2^-43 of that magnitude below.  Sums and softmax
+ * statistics are fp32; P is rounded to bf16.
  * Masked scores never reach the sums, whatever the cache holds there; values of V at
  * positions below kv_len[b] have to be finite in the rows' visible 128-key tiles.  An
  * infinite query value counts as NaN over an e4m3 cache.

@@ -30,12 +30,16 @@
 // the others come from the 16 KB behind the V tile and are never read.
 //
 // e4m3 cache.  K goes to the tensor cores as it lies (no widening: half of that work and of
-// its shared-memory traffic), so Q has to be 8-bit too, without losing anything: a bf16
-// value has 8 significant bits, e4m3 has 4, and q 2^-e = hi + lo with hi its nearest e4m3
-// and lo the rest.  With e from the row's largest magnitude (at most 448 2^e) the sum is
-// exact for values down to 2^-10 of it and off by at most 2^-18 of it below.  hi and lo are
+// its shared-memory traffic), so Q has to be 8-bit too, without losing anything.  A bf16 value
+// has 8 significant bits, e4m3 has 4, and e4m3 ends at 2^-9 where a query row may have any
+// range, so q 2^-e (e from the row's largest magnitude, at most 448 2^e) goes as four parts:
+//     q 2^-e = p0 + 2^-4 (p1 + 2^-18 (p2 + 2^-4 p3)),
+// each the nearest e4m3 of what the parts before it left.  p0 takes 4 bits, p1 the 4 below them:
+// exact down to 2^-6, from where what is left (at most 2^-10 in units of p1) starts again at
+// p2's 256.  So a value is exact down to 2^-35 of its row's largest magnitude and off by at
+// most 2^-43 of it below.  (Two parts, p1 unscaled, lose bits from 2^-10 of it on.)  The parts are
 // columns of the same product (the MMA thread, which issues 8 small instructions per P V,
-// bounds an e4m3 tile, so S should take few), and the softmax thread adds the two; the scales
+// bounds an e4m3 tile, so S should take few), and the softmax thread adds them up; the scales
 // 2^e of a query row and of its key multiply the sum.  V is widened to bf16, as its products
 // with P need.
 #pragma once
@@ -54,13 +58,13 @@ struct FewCfg {
   static constexpr int kBox = 128 * 128;
   static constexpr int NB = D / 64;                // 64-column boxes of a bf16 tile
   static constexpr int kKTile = K8 ? 128 * 128 : kTile;
-  static constexpr int kQBox = NQ * 128;
+  static constexpr int kQBox = (K8 ? (NR < 8 ? 8 : NR) : NQ) * 128;    // K8: read by the split only
   static constexpr int kQTile = NB * kQBox;
-  static constexpr int kPTile = 2 * kQBox;         // P^T: NQ rows of 128 keys
+  static constexpr int kPBox = NQ * 128;
+  static constexpr int kPTile = 2 * kPBox;         // P^T: NQ rows of 128 keys
   static constexpr int QST = 2;
-  static constexpr int NH = NR < 8 ? 8 : NR;       // K8: rows 0 .. NR - 1 hi parts of Q, from NH on lo parts
-  static constexpr int NS = K8 ? 2 * NH : NQ;      // columns of S^T
-  static constexpr int kQ8 = K8 ? NS * 128 : 0;    // both parts, 128-byte rows
+  static constexpr int NS = K8 ? 4 * NR : NQ;      // columns of S^T; K8: part i of row r in column i NR + r
+  static constexpr int kQ8 = K8 ? NS * 128 : 0;    // the parts, 128-byte rows
   static constexpr int KSK = K8 ? 4 : D == 128 ? 3 : 6;
   static constexpr int KSV = KV8 ? (D == 128 ? 2 : 3) : KSK;
   // S(g) completes behind PV(g - SA), so P(g) may take the buffer of P(g - NP) for NP >= SA
@@ -177,10 +181,29 @@ __device__ __forceinline__ void few_tmem_st(uint32_t addr, const float (&f)[NR])
   else tmem_st16(addr, r);
 }
 
+// Scale between part i of Q and part i + 1 (see the head of this file).
+__host__ __device__ constexpr float few_part_step(int i) { return i == 1 ? 262144.f : 16.f; }
+
+// Scores of this thread's key from the four parts of Q, smallest first: 16 columns per trip to TMEM.
+template <int NR>
+__device__ __forceinline__ void few_scores(uint32_t addr, float (&x)[NR]) {
+  constexpr int PER = 16 / NR;                       // parts per trip
+#pragma unroll
+  for (int part = 4 - PER; part >= 0; part -= PER) {
+    float t[16];
+    few_tmem_ld<16>(addr + part * NR, t);
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i)
+#pragma unroll
+      for (int q = 0; q < NR; ++q)
+        x[q] = part + i == 3 ? t[i * NR + q] : fmaf(x[q], 1.f / few_part_step(part + i), t[i * NR + q]);
+  }
+}
+
 // 2^(byte - 127), also for byte 0 (subnormal).
 __device__ __forceinline__ float e8m0_value(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
 
-// Q of a piece as hi + lo parts (see the head of this file), row scales to cq.
+// Q of a piece in four e4m3 parts (see the head of this file), row scales to cq.
 template <class C>
 __device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float* cq, int wt) {
   constexpr int CPR = C::D / 8;                      // 8-value chunks per row, one per lane
@@ -199,26 +222,27 @@ __device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float
     for (int m = CPR / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
     const int e = e4m3_exponent(amax);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[2], v[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float a = f[4 * h + 2 * k] * inv, b = f[4 * h + 2 * k + 1] * inv;
-        if (!(fabsf(a) < INFINITY)) a = NAN;         // an infinite query value gives no finite score
-        if (!(fabsf(b) < INFINITY)) b = NAN;
-        w[k] = pack_e4m3x2(a, b);
-        const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[k]), __NV_E4M3);
-        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        v[k] = pack_e4m3x2(a - g.x, b - g.y);
-      }
-      hi[h] = w[0] | (w[1] << 16);
-      lo[h] = v[0] | (v[1] << 16);
+    for (int i = 0; i < 8; ++i) {
+      f[i] *= inv;
+      if (!(fabsf(f[i]) < INFINITY)) f[i] = NAN;     // an infinite query value gives no finite score
     }
-    const int off = r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-    *reinterpret_cast<uint2*>(q8 + off) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(q8 + C::NH * 128 + off) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+    for (int part = 0; part < 4; ++part) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t two = pack_e4m3x2(f[i], f[i + 1]);
+        const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        f[i] = (f[i] - g.x) * few_part_step(part);
+        f[i + 1] = (f[i + 1] - g.y) * few_part_step(part);
+        w[i >> 1] = two;
+      }
+      const int pr = part * C::NR + r;
+      *reinterpret_cast<uint2*>(q8 + pr * 128 + (((c >> 1) ^ (pr & 7)) << 4) + (c & 1) * 8) =
+          make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    }
     if (c == 0) cq[r] = e8m0_value(static_cast<uint32_t>(e + 127));
   }
 }
@@ -320,7 +344,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
           const uint32_t d = tmem + C::kO + (g & 1) * NQ;
 #pragma unroll
           for (int k2 = 0; k2 < 8; ++k2)
-            umma_ss_lo(d, v_lo + ((k2 * 2048) >> 4), p_lo + (((k2 >> 2) * C::kQBox + (k2 & 3) * 32) >> 4), hi, idO,
+            umma_ss_lo(d, v_lo + ((k2 * 2048) >> 4), p_lo + (((k2 >> 2) * C::kPBox + (k2 & 3) * 32) >> 4), hi, idO,
                        !(j < 2 && k2 == 0));
           umma_commit(&sh.v_done[g & 7]);
           if (j + C::SA < w.n) ok = issue_s(g + C::SA);
@@ -347,7 +371,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
     const int row = wq * 32 + lane;                             // key of the tile, column of O
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const bool has_o = wq * 32 < D;                             // d = 64: the first two warps hold O
-    uint8_t* prow = sP + (row >> 6) * C::kQBox + (row & 7) * 2;
+    uint8_t* prow = sP + (row >> 6) * C::kPBox + (row & 7) * 2;
     const int chunk = ((row & 63) >> 3) << 4;
     int gs = 0, uq = 0, fs = 0;                                 // steps, pieces, raised bases
     bool ok = true;
@@ -376,13 +400,11 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float x[NR];
-        few_tmem_ld<NR>(lane_base + (g & 3) * C::NS, x);
         float c = p.cs;
-        if constexpr (KV8) {
-          float lo[NR];
-          few_tmem_ld<NR>(lane_base + (g & 3) * C::NS + C::NH, lo);
-#pragma unroll
-          for (int q = 0; q < NR; ++q) x[q] += lo[q];
+        if constexpr (!KV8) {
+          few_tmem_ld<NR>(lane_base + (g & 3) * C::NS, x);
+        } else {
+          few_scores<NR>(lane_base + (g & 3) * C::NS, x);
           // this key's scale; the floor (below any that matters) keeps -inf times c at -inf
           c = fmaxf(c * e8m0_value(m.kscale[(g & 7) * 128 + row]), 1e-37f);
 #pragma unroll

@@ -61,3 +61,51 @@ def test_outputs_on_a_side_stream_are_not_memory_that_others_still_write(attn): 
         torch.cuda.synchronize()
         ok(attn)
         assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+# ------------------------------------------------------------------ queries of wide range
+FEW = [   # Hq / Hkv, tokens per sequence: every build of the kernel for few rows, then one of the 128-row kernel
+    (1, 1), (4, 1), (2, 3), (8, 1), (3, 5), (16, 1)]
+
+
+@pytest.mark.parametrize("wide", [0, 10, 13, 17, 27])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", FEW)
+def test_small_channels_of_a_wide_query_keep_their_bits_over_e4m3(attn, G, n, d, wide):  # noqa: F811
+    """One channel of Q 2^wide times the others, where K is small (codes of 0 to 3 units of 2^-9; all
+    zero at 2^27): the others decide the scores and must not lose bits to the large one."""
+    B, Hkv, page, lens = 2, 2, 32, [300, 129]
+    pool = Pool(B, Hkv, page, d, lens, True, seed=wide + d)
+    g = torch.Generator().manual_seed(9)
+    small = torch.randint(0, 4 if wide < 20 else 1, pool.store["k"].shape[:3], generator=g).to(torch.uint8)
+    own = pool.store["k"][..., 5] != 0x7f
+    pool.store["k"][..., 5] = torch.where(own, small, pool.store["k"][..., 5])
+    pool.value["k"] = ref.widened(pool.store["k"], pool.store["ks"])
+    q = normal((B * n, G * Hkv, d), 3 + G)
+    q[..., 5] = (q[..., 5].float().abs() + 0.5).mul(2.0 ** wide).to(torch.bfloat16)
+    where, scales = pool.cuda()
+    got = attn.attn_paged(q.cuda(), *where, bounds([n] * B).cuda(), ints(lens).cuda(), **scales)
+    ok(attn)
+    check_attention(got, ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([n] * B), lens, d ** -0.5))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_answer_over_e4m3_does_not_depend_on_the_rows_of_the_call(attn, d):  # noqa: F811
+    """The same wide query alone (few rows) and beside 200 other tokens (the 128-row kernel).  Both round
+    P and O once: they differ by two roundings of each at most."""
+    Hq, Hkv, page, L = 4, 1, 64, 700
+    pool = Pool(2, Hkv, page, d, [L, 200], True, seed=d)
+    pool.store["k"][..., 9] = torch.where(pool.store["k"][..., 9] != 0x7f, 1, pool.store["k"][..., 9])
+    pool.value["k"] = ref.widened(pool.store["k"], pool.store["ks"])
+    q = normal((201, Hq, d), 4)
+    q[..., 9] = (q[..., 9].float() * 2.0 ** 15).to(torch.bfloat16)
+    (kc, vc, table), scales = pool.cuda()
+    one = attn.attn_paged(q[:1].cuda(), kc, vc, table[:1].contiguous(), bounds([1]).cuda(), ints([L]).cuda(), **scales)
+    many = attn.attn_paged(q.cuda(), kc, vc, table, bounds([1, 200]).cuda(), ints([L, 200]).cuda(), **scales)
+    ok(attn)
+    wo, wl, wabs = ref.attend(q[:1], pool.value["k"], pool.value["v"], pool.table, bounds([1]), [L], d ** -0.5)
+    check_attention(one, (wo, wl, wabs))
+    assert float((one[1] - many[1][:1]).abs().max()) <= 1e-3
+    u = 2.0 ** -8
+    diff = (one[0].cpu().double() - many[0][:1].cpu().double()).abs()
+    assert bool((diff <= 2 * ((u + 2e-4) * wabs + u * wo.abs()) + 1e-6).all())
