@@ -400,17 +400,20 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float x[NR];
-        float c = p.cs;
+        // Scores in the exponent's units.  They are masked afterwards: no factor meets a -inf.
         if constexpr (!KV8) {
           few_tmem_ld<NR>(lane_base + (g & 3) * C::NS, x);
+#pragma unroll
+          for (int q = 0; q < NR; ++q) x[q] *= p.cs;
         } else {
           few_scores<NR>(lane_base + (g & 3) * C::NS, x);
-          // this key's scale; the floor (below any that matters) keeps -inf times c at -inf
-          c = fmaxf(c * e8m0_value(m.kscale[(g & 7) * 128 + row]), 1e-37f);
+          // The scales of key and row are multiplied first: a large one and a small one cancel
+          // before either meets the sum, which alone can pass fp32 with the row's.
+          const float c = p.cs * e8m0_value(m.kscale[(g & 7) * 128 + row]);
 #pragma unroll
           for (int q = 0; q < NR; q += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&sh.cq[uq & 3][q]);
-            x[q] *= f.x; x[q + 1] *= f.y; x[q + 2] *= f.z; x[q + 3] *= f.w;
+            x[q] *= f.x * c; x[q + 1] *= f.y * c; x[q + 2] *= f.z * c; x[q + 3] *= f.w * c;
           }
         }
         const int k0 = (w.j0 + g - gs) * 128, key = k0 + row;
@@ -426,10 +429,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
           }
         }
 #pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          x[q] *= c;
-          up |= x[q] > mu[q] + kRescaleTau;
-        }
+        for (int q = 0; q < NR; ++q) up |= x[q] > mu[q] + kRescaleTau;
         up = __any_sync(0xffffffffu, up);
         if (lane == 0) sh.vote[x2][par][wq] = up;
         ok = group_sync(&sh.vbar[x2][par], (g >> 2) & 1);

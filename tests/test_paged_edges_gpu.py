@@ -109,3 +109,25 @@ def test_an_answer_over_e4m3_does_not_depend_on_the_rows_of_the_call(attn, d):  
     u = 2.0 ** -8
     diff = (one[0].cpu().double() - many[0][:1].cpu().double()).abs()
     assert bool((diff <= 2 * ((u + 2e-4) * wabs + u * wo.abs()) + 1e-6).all())
+
+
+@pytest.mark.parametrize("power,byte", [(119, 3), (-110, 230)])
+@pytest.mark.parametrize("G,n", FEW)
+def test_huge_and_tiny_scales_cancel_over_e4m3(attn, G, n, power, byte):  # noqa: F811
+    """Queries of 2^power against keys of about 2^-power: scores of a few units, though the sum of
+    codes and one of the two scales alone can leave fp32's range."""
+    B, Hkv, d, page, lens = 2, 2, 128, 16, [300, 129]
+    pool = Pool(B, Hkv, page, d, lens, True, seed=G + n)
+    codes = pool.store["k"]
+    codes[(codes & 0x78) <= 0x68] += 16                        # four times the value; NaN stays
+    pool.store["ks"] = pool.store["ks"] - 119 + byte           # byte .. byte + 4
+    pool.value["k"] = ref.widened(codes, pool.store["ks"])
+    q = (normal((B * n, G * Hkv, d), 3 + G, torch.float32) * 2.0 ** power).to(torch.bfloat16)
+    where, scales = pool.cuda()
+    scale = d ** -0.5 / 32                                     # sums of sizes up to 13: the tolerance holds
+    got = attn.attn_paged(q.cuda(), *where, bounds([n] * B).cuda(), ints(lens).cuda(), **scales, scale=scale)
+    ok(attn)
+    want = ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([n] * B), lens, scale)
+    finite = want[1][~torch.isinf(want[1])]
+    assert bool((finite.abs() < 30).all())                     # the case is one of ordinary scores
+    check_attention(got, want)
