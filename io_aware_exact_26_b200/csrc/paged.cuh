@@ -487,8 +487,10 @@ struct PageWindow {
   }
 };
 
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src))
+// Four bytes, of which the first `bytes` come from src (nothing is read for 0) and the rest are 0.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
                : "memory");
 }
 // Arrive on the barrier once this thread's cp.async so far have landed (one of its count).
@@ -531,12 +533,17 @@ __device__ __forceinline__ bool paged_load_tiles(const PagedParams& p, PagedPipe
     const int st = c % kStages, round = c / kStages;
     uint64_t* full = kRaw ? &sh.raw_full[st] : kv == 0 ? &sh.k_full[st] : &sh.v_full[st];
     uint8_t* dst = kRaw ? m.raw + st * C::kRawTile : kv == 0 ? m.k + st * C::kKTile : m.v + st * C::kTile;
-    const uint8_t* scale_src = nullptr;             // scale bytes of rows 4 lane .. 4 lane + 3
+    // Scale bytes of rows 4 lane .. 4 lane + 3.  Rows that are not followed get 0 like their codes,
+    // not what the slot held: 0 times a stale factor of infinity would be NaN.
+    const uint8_t* scale_src = kv ? p.c.vs : p.c.ks;
+    int scale_bytes = 0;
     if constexpr (C::KV8) {
       const int r = 4 * lane, box = (r >> psh) - t.first;
       const int pg = __shfl_sync(0xffffffffu, page, box & 31);                // lane i holds the page of box i
-      if (box >= 0 && box < t.count && pg >= 0)
-        scale_src = (kv ? p.c.vs : p.c.ks) + (((static_cast<long long>(pg) * p.Hkv + w.g) << shift) + y + (r & (rows - 1)));
+      if (box >= 0 && box < t.count && pg >= 0) {
+        scale_src += ((static_cast<long long>(pg) * p.Hkv + w.g) << shift) + y + (r & (rows - 1));
+        scale_bytes = 4;
+      }
     }
     if (round > 0) {
       const bool free = kRaw ? mbar_wait(&sh.raw_empty[st], (round - 1) & 1)
@@ -556,7 +563,7 @@ __device__ __forceinline__ bool paged_load_tiles(const PagedParams& p, PagedPipe
     }
     if constexpr (C::KV8) {
       uint8_t* scale = kRaw ? m.scale + st * 128 : m.kscale + (kc & 7) * 128;
-      if (scale_src) cp_async4(scale + 4 * lane, scale_src);
+      cp_async4(scale + 4 * lane, scale_src, scale_bytes);
       cp_async_arrive(full);
     }
   }

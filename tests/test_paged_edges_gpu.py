@@ -131,3 +131,24 @@ def test_huge_and_tiny_scales_cancel_over_e4m3(attn, G, n, power, byte):  # noqa
     finite = want[1][~torch.isinf(want[1])]
     assert bool((finite.abs() < 30).all())                     # the case is one of ordinary scores
     check_attention(got, want)
+
+
+# ------------------------------------------------------------------ pages that are not followed
+@pytest.mark.parametrize("Hq", [1, 8, 16, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_pages_over_e4m3_count_as_zeros_whatever_was_loaded_before(attn, d, Hq):  # noqa: F811
+    """3000 one-page sequences, some 20 to an SM: eight of good pages under the scale byte 255
+    (infinity), then eight whose table entry is no page.  The latter see 16 keys of zeros."""
+    B, page = 3000, 16
+    kc, vc = (torch.ones(2, 1, page, d, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.full((2, 1, page), 255, dtype=torch.uint8, device="cuda") for _ in range(2))
+    b = torch.arange(B)
+    bad = (b // 8) % 2 == 1
+    table = torch.where(bad, torch.where(b % 2 == 0, -1, 2), b % 2).to(torch.int32).reshape(B, 1).cuda()
+    q = normal((B, Hq, d), 3).cuda()
+    o, lse = attn.attn_paged(q, kc, vc, table, torch.arange(B + 1, dtype=torch.int32, device="cuda"),
+                             torch.full((B,), page, dtype=torch.int32, device="cuda"), k_scale=ks, v_scale=vs)
+    assert attn.attn_get_device_status() == -10
+    assert bool((o.cpu()[bad] == 0).all())
+    assert float((lse.cpu()[bad] - math.log(page)).abs().max()) <= 1e-5
+    ok(attn)
