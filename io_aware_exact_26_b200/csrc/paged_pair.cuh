@@ -272,21 +272,24 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
           for (int kk = 0; kk < 16; kk += 8) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              mx4[e] = max3f(mx4[e], __uint_as_float(r0[kk + e]), __uint_as_float(r0[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r1[kk + e]), __uint_as_float(r1[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r2[kk + e]), __uint_as_float(r2[kk + e + 4]));
-              mx4[e] = max3f(mx4[e], __uint_as_float(r3[kk + e]), __uint_as_float(r3[kk + e + 4]));
+              mx4[e] = max3f_nan(mx4[e], __uint_as_float(r0[kk + e]), __uint_as_float(r0[kk + e + 4]));
+              mx4[e] = max3f_nan(mx4[e], __uint_as_float(r1[kk + e]), __uint_as_float(r1[kk + e + 4]));
+              mx4[e] = max3f_nan(mx4[e], __uint_as_float(r2[kk + e]), __uint_as_float(r2[kk + e + 4]));
+              mx4[e] = max3f_nan(mx4[e], __uint_as_float(r3[kk + e]), __uint_as_float(r3[kk + e + 4]));
             }
           }
         }
-        sh.xmax[x][xp][grp][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        sh.xmax[x][xp][grp][row] = max3f_nan(max3f_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.xbar[x][xp][quad]);
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.xbar[x][xp][quad], (xs >> 1) & 1));
         if (!ok) break;
         ++xs;
-        const float mx = fmaxf(sh.xmax[x][xp][0][row], sh.xmax[x][xp][1][row]);
+        const float mx = max3f_nan(sh.xmax[x][xp][0][row], sh.xmax[x][xp][1][row], -INFINITY);
         const float m_tile = mx == -INFINITY ? -INFINITY : mx * c;
+        // A row that sees a NaN or an infinite score is NaN.  It has to say so by its base: the
+        // polynomial would turn the one NaN into a small weight, on its columns and no others.
+        if (!(m_tile < INFINITY)) m_used = NAN;
         float alpha = 1.f;
         const bool need = valid && m_tile > m_used + kRescaleTau;
         if (need) {

@@ -427,6 +427,13 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return m;
 }
 
+// The same, NaN where one of them is.
+__device__ __forceinline__ float max3f_nan(float a, float b, float c) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+
 // Packed pairs of fp32 (sm_100 f32x2 arithmetic): two lanes of work per instruction.
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
   uint64_t r;

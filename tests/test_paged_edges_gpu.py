@@ -152,3 +152,32 @@ def test_bad_pages_over_e4m3_count_as_zeros_whatever_was_loaded_before(attn, d, 
     assert bool((o.cpu()[bad] == 0).all())
     assert float((lse.cpu()[bad] - math.log(page)).abs().max()) <= 1e-5
     ok(attn)
+
+
+# ------------------------------------------------------------------ values that are not finite, or huge
+FORMS = [(4, 1), (2, 20), (2, 100)]         # Hq / Hkv, tokens: the kernels for few rows, 128 rows, two tiles of 128
+
+
+@pytest.mark.parametrize("e4m3,bad", [(False, math.nan), (False, math.inf), (True, math.nan)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", FORMS)
+def test_a_key_that_is_not_finite_reaches_the_rows_that_see_it_and_no_others(attn, G, n, d, e4m3, bad):  # noqa: F811
+    """16 sequences with such a value in one channel of the key at one of 16 successive positions, so at
+    every column of a softmax thread's loop.  Rows that see it are NaN, or for a score of -inf
+    free of it, as the definition says; the others are untouched."""
+    B, Hkv, page, L = 16, 1, 32, 300
+    pool = Pool(B, Hkv, page, d, [L] * B, e4m3, seed=d + n)
+    for b in range(B):
+        p = 230 + b
+        at = (int(pool.table[b, p // page]), 0, p % page, 11)
+        pool.store["k"][at] = 0x7f if e4m3 else bad
+    pool.value["k"] = ref.widened(pool.store["k"], pool.store["ks"]) if e4m3 else pool.store["k"].double()
+    q = normal((B * n, G, d), 5)
+    where, scales = pool.cuda()
+    o, lse = (x.cpu().double() for x in attn.attn_paged(q.cuda(), *where, bounds([n] * B).cuda(), ints([L] * B).cuda(), **scales))
+    ok(attn)
+    wo, wl, wabs = ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([n] * B), [L] * B, d ** -0.5)
+    seen = wo.isnan().any(-1)                              # [T, Hq]
+    assert bool(seen.any()) and torch.equal(o.isnan().all(-1), seen) and torch.equal(o.isnan().any(-1), seen)
+    assert bool((~lse[seen].isfinite()).all())
+    check_attention((o[~seen], lse[~seen]), (wo[~seen], wl[~seen], wabs[~seen]))
