@@ -332,7 +332,10 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
             float x0, x1, a, b;
             f2unpack(xx, x0, x1);
             if (kk >= 8 - C::kFmaPairs) {
-              exp2_fma_pair(x0, x1, a, b);      // -inf gives 2^-126.5: nothing beside the row's other terms
+              exp2_fma_pair(x0, x1, a, b);
+              // it ends at 2^-127, which is something beside a masked value of 2^127: 0 as below
+              a = x0 < -126.f ? 0.f : a;
+              b = x1 < -126.f ? 0.f : b;
             } else {
               a = ex2_approx(x0);
               b = ex2_approx(x1);
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(PairCfg<D>::kThreads, 1)
       if (active) {
         tc_fence_after();
         const float l = sh.xsum[x][0][row] + sh.xsum[x][1][row];
-        const bool none = m_used == -INFINITY && l == l;        // no key seen (l holds 2^-126.5 terms, or NaN scores)
+        const bool none = l == 0.f;                             // no key seen
         const float inv_l = none ? 0.f : 1.f / l;
         const bool okrow = valid && in_range(w.tok0 + it, p.T) && in_range(x * p.G * p.R + row, w.slot < 0 ? 256 : p.slot_rows);
         if (w.slot < 0) {

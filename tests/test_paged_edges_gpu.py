@@ -181,3 +181,35 @@ def test_a_key_that_is_not_finite_reaches_the_rows_that_see_it_and_no_others(att
     assert bool(seen.any()) and torch.equal(o.isnan().all(-1), seen) and torch.equal(o.isnan().any(-1), seen)
     assert bool((~lse[seen].isfinite()).all())
     check_attention((o[~seen], lse[~seen]), (wo[~seen], wl[~seen], wabs[~seen]))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", FORMS)
+def test_huge_values_at_masked_positions_do_not_leak(attn, G, n, d, e4m3):  # noqa: F811
+    """V of the type's largest magnitude at every position that a row does not see (later new tokens,
+    positions before the window) must add nothing: the rows that see none of it agree with the
+    definition to their own tolerance."""
+    B, Hkv, page, L, window = 3, 1, 32, 400, 60
+    pool = Pool(B, Hkv, page, d, [L] * B, e4m3, seed=d + n)
+    first = L - n
+    far = first - window                                   # the first row's window begins here
+    huge = list(range(far - 30, far)) + list(range(first + 1, L))     # the first row sees none of them
+    for b in range(B):
+        for p in huge:
+            at = (int(pool.table[b, p // page]), slice(None), p % page)
+            if e4m3:
+                pool.store["v"][at] = 0x7e                 # 448 under the largest scale the write makes
+                pool.store["vs"][at] = 247 - 1
+            else:
+                pool.store["v"][at] = torch.finfo(torch.bfloat16).max * (-1) ** p
+    pool.value["v"] = ref.widened(pool.store["v"], pool.store["vs"]) if e4m3 else pool.store["v"].double()
+    q = normal((B * n, G, d), 5)
+    where, scales = pool.cuda()
+    o, lse = (x.cpu() for x in attn.attn_paged(q.cuda(), *where, bounds([n] * B).cuda(), ints([L] * B).cuda(), **scales,
+                                               window_left=window))
+    ok(attn)
+    want = ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([n] * B), [L] * B, d ** -0.5, True, window)
+    rows = torch.arange(0, B * n, n)                       # of each sequence the first
+    check_attention((o[rows], lse[rows]), tuple(x[rows] for x in want))
+    assert float(want[0][rows].abs().max()) < 10
