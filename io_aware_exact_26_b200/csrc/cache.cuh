@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(256) attn_cache_write_kernel(const WriteParams
   bool live = tok < p.T && b < p.B;
   int pos = 0;
   if (live) {
-    pos = p.kv_len[b] - p.cu_q[b + 1] + t;
+    pos = max(0, p.kv_len[b]) - p.cu_q[b + 1] + t;      // a negative length counts as 0
     live = pos >= 0 && t >= p.cu_q[b];          // (rows before cu_q[0] belong to nobody)
   }
   const RopeUnit<T, D, INTER> unit(u, p.inv_freq ? p.rot : 0);

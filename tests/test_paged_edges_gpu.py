@@ -213,3 +213,33 @@ def test_huge_values_at_masked_positions_do_not_leak(attn, G, n, d, e4m3):  # no
     rows = torch.arange(0, B * n, n)                       # of each sequence the first
     check_attention((o[rows], lse[rows]), tuple(x[rows] for x in want))
     assert float(want[0][rows].abs().max()) < 10
+
+
+# ------------------------------------------------------------------ lengths
+@pytest.mark.parametrize("length", [-1, -5, -(1 << 30), -(1 << 31)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_negative_length_counts_as_zero(attn, length, e4m3):  # noqa: F811
+    """Nothing is written, read or attended to for that sequence and nothing is reported; the other one's
+    results are those of the call alone."""
+    Hq, Hkv, d, page, L, n = 4, 2, 64, 16, 40, 3
+    pool = Pool(1, Hkv, page, d, [L], e4m3, seed=3)
+    (kc, vc, table), scales = pool.cuda()
+    rows = normal((2 * n, Hq + 2 * Hkv, d), 4).cuda()
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    kc2, vc2 = kc.clone(), vc.clone()
+    sc2 = {m: x.clone() for m, x in scales.items()}
+    alone = (bounds([n]).cuda(), ints([L]).cuda())
+    both = (bounds([n, n]).cuda(), ints([L, length]).cuda())
+    t2 = table.repeat(2, 1).contiguous()
+    attn.attn_cache_write(k[:n], v[:n], kc, vc, table, *alone, **scales)
+    attn.attn_cache_write(k, v, kc2, vc2, t2, *both, **sc2)
+    ok(attn)
+    for a, b in [(kc, kc2), (vc, vc2)] + [(scales[m], sc2[m]) for m in scales]:
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    want = attn.attn_paged(q[:n], kc, vc, table, *alone, **scales)
+    got = attn.attn_paged(q, kc, vc, t2, *both, **scales)
+    kr, vr = attn.attn_cache_read(kc, vc, t2, both[1], N=L, **scales)
+    ok(attn)
+    assert all(torch.equal(g[:n], w) for g, w in zip(got, want))
+    assert bool((got[0][n:] == 0).all()) and bool(torch.isinf(got[1][n:]).all())
+    assert bool((kr[1] == 0).all()) and bool((vr[1] == 0).all())
