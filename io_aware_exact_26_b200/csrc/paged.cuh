@@ -93,11 +93,12 @@ struct PagedSeq {
     tok0 = p.cu_q[b];
     const int end = min(p.cu_q[b + 1], p.T);
     nq = tok0 >= 0 ? max(0, end - tok0) : 0;
-    // no further than the table leads: what lies behind is reported and not followed
+    // no further than the table leads: what lies behind is not followed and, where rows would see
+    // it, reported (a slot without new tokens may hold any length)
     const long long room = static_cast<long long>(p.max_pages) << p.c.page_shift;
     len = max(0, p.kv_len[b]);
     if (len > room) {
-      record_bad_page();
+      if (nq > 0) record_bad_page();
       len = static_cast<int>(room);
     }
     // positions follow from the sequence's own count of tokens, also where T cuts it short

@@ -243,3 +243,16 @@ def test_a_negative_length_counts_as_zero(attn, length, e4m3):  # noqa: F811
     assert all(torch.equal(g[:n], w) for g, w in zip(got, want))
     assert bool((got[0][n:] == 0).all()) and bool(torch.isinf(got[1][n:]).all())
     assert bool((kr[1] == 0).all()) and bool((vr[1] == 0).all())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_a_slot_without_tokens_is_not_reported_for_its_length(attn, T):  # noqa: F811
+    """Slots that wait (no new token) may hold any length: no row sees a position behind their table."""
+    Hq, Hkv, d, page, L = 4, 2, 64, 16, 330
+    pool = Pool(1, Hkv, page, d, [L], False, seed=3)
+    (kc, vc, table), _ = pool.cuda()
+    q = normal((T, Hq, d), 4)
+    got = attn.attn_paged(q.cuda(), kc, vc, table.repeat(3, 1).contiguous(), bounds([0, T, 0]).cuda(),
+                          ints([1 << 29, L, page * table.shape[1] + 1]).cuda())
+    ok(attn)
+    check_attention(got, ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([T]), [L], d ** -0.5))
