@@ -256,3 +256,118 @@ def test_a_slot_without_tokens_is_not_reported_for_its_length(attn, T):  # noqa:
                           ints([1 << 29, L, page * table.shape[1] + 1]).cuda())
     ok(attn)
     check_attention(got, ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([T]), [L], d ** -0.5))
+
+
+# ------------------------------------------------------------------ running maxima
+@pytest.mark.parametrize("order", ["rising", "falling", "one"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", FEW + [(2, 20), (2, 100)])
+def test_maxima_that_move_from_tile_to_tile(attn, G, n, d, e4m3, order):  # noqa: F811
+    """Scores that grow or shrink along the keys into the hundreds, or one key far above the rest: every
+    kernel raises its exponent base and rescales, or never again, in each of its shares.  An fp32
+    score of 128 products is off by at most 2^-17 of the sum of their sizes; weights follow it."""
+    B, Hkv, page, lens = 2, 2, 32, [900, 517]
+    pool = Pool(B, Hkv, page, d, lens, e4m3, seed=d + G)
+    for b, L in enumerate(lens):
+        for p in range(L):
+            at = (int(pool.table[b, p // page]), slice(None), p % page)
+            far = p if order == "rising" else L - 1 - p
+            step = (8 if p == L // 2 else 1) if order == "one" else far // 64
+            if e4m3:
+                pool.store["ks"][at] = 119 + step if order == "one" else 114 + step
+            else:
+                pool.store["k"][at] = (pool.store["k"][at].float() * (step if order == "one" else 0.5 + step)).to(torch.bfloat16)
+    for m in "kv":
+        pool.value[m] = ref.widened(pool.store[m], pool.store[m + "s"]) if e4m3 else pool.store[m].double()
+    q = (normal((B * n, G * Hkv, d), 13).float() * 3).to(torch.bfloat16)
+    where, scales = pool.cuda()
+    o, lse = (x.cpu().double() for x in attn.attn_paged(q.cuda(), *where, bounds([n] * B).cuda(), ints(lens).cuda(), **scales))
+    ok(attn)
+    wo, wl, wabs = ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([n] * B), lens, d ** -0.5)
+    u, size = 2.0 ** -8, 0.0
+    for b, L in enumerate(lens):
+        k = ref.gathered(pool.value["k"], pool.table[b], L).abs().repeat_interleave(G, 0)
+        size = max(size, float(torch.einsum("thd,hkd->thk", q[b * n:(b + 1) * n].double().abs(), k).max()) * d ** -0.5)
+    s = 2.0 ** -17 * size
+    assert bool(((o - wo).abs() <= (u + 2e-4 + 2 * s) * wabs + u * wo.abs() + 1e-6).all())
+    # beside the scores' error: exp2 and log2 by a few 2^-22, and the 2^-24 of a value of wl's size
+    assert float(((lse - wl).abs() - 2.0 ** -22 * wl.abs()).max()) <= s + 1e-5
+    assert size < 4000
+
+
+# ------------------------------------------------------------------ far addresses, broadcast views
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_pool_beyond_32_bit_offsets(attn, e4m3):  # noqa: F811
+    """Pages on both sides of 2^32 bytes and, for bf16, of 2^31 elements: written, read back, attended to by each
+    kernel."""
+    Hq, Hkv, page, d, L = 16, 8, 64, 128, 450
+    room = Hkv * page * d
+    pages = 2 ** 32 // (room * (1 if e4m3 else 2)) + 40
+    shape = (pages, Hkv, page, d)
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = (torch.empty(shape, dtype=dt, device="cuda") for _ in range(2))
+    sc = {m: torch.empty(shape[:3], dtype=torch.uint8, device="cuda") for m in ("k_scale", "v_scale")} if e4m3 else {}
+    table = ints([[pages - 1, 0, pages // 2 - 1, pages // 2, pages - 2, 3, pages - 40, pages - 41]]).cuda()
+    k, v, q = (normal((L, H, d), H + i) for i, H in enumerate((Hkv, Hkv, Hq)))
+    kv_len = ints([L]).cuda()
+    attn.attn_cache_write(k.cuda(), v.cuda(), kc, vc, table, bounds([L]).cuda(), kv_len, **sc)
+    kr, vr = attn.attn_cache_read(kc, vc, table, kv_len, N=L, **sc)
+    ok(attn)
+    if not e4m3:
+        assert torch.equal(kr[0].transpose(0, 1).cpu(), k) and torch.equal(vr[0].transpose(0, 1).cpu(), v)
+    else:
+        assert float((kr[0].transpose(0, 1).cpu().double() - k.double()).abs().max()) <= 4 * 2.0 ** -4
+    dense, one = (x.cpu().double() for x in (kr, vr)), torch.zeros(1, 1, dtype=torch.int32)
+    dense = list(dense)
+    for n in (1, 8, 40, L):
+        got = attn.attn_paged(q[L - n:].cuda(), kc, vc, table, bounds([n]).cuda(), kv_len, **sc)
+        ok(attn)
+        check_attention(got, ref.attend(q[L - n:], *dense, one, bounds([n]), [L], d ** -0.5))
+    del kc, vc, sc
+    torch.cuda.empty_cache()
+
+
+def test_rotation_and_read_back_beyond_2_31_elements(attn):  # noqa: F811
+    """Tensors of more than 2^31 elements, compared at their two ends and around the border."""
+    H, d, N = 128, 128, 2 ** 31 // (128 * 128) + 300
+    x = torch.empty(1, H, N, d, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    f = attn.rope_inv_freq(d)[0]
+    y, _ = attn.attn_rope(x, positions=pos, inv_freq=f)
+    packed, _ = attn.attn_rope(x.reshape(N, H, d), positions=pos, inv_freq=f)
+    ok(attn)
+    at = torch.tensor([0, 1, N // 2, N - 301, N - 300, N - 299, N - 1])
+    for h in (0, 1, H - 1):
+        want = ref.rotate(x[0, h, at].cpu().unsqueeze(1), at, f.cpu(), False).squeeze(1)
+        assert bool(((y[0, h, at].cpu().double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all())
+        want = ref.rotate(x.reshape(N, H, d)[at, h].cpu().unsqueeze(1), at, f.cpu(), False).squeeze(1)
+        assert bool(((packed[at, h].cpu().double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all())
+    del y, packed, x
+    B, Hkv, L, page = 64, 4, 40, 16
+    pool = Pool(B, Hkv, page, d, [L] * B, False, seed=2)
+    where, _ = pool.cuda()
+    N = 2 ** 31 // (B * Hkv * d) + 9
+    k, v = (torch.empty(B, Hkv, N, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    attn.attn_cache_read(*where, ints([L] * B).cuda(), k_out=k, v_out=v)
+    ok(attn)
+    for b in range(B):
+        for got, n in ((k, "k"), (v, "v")):
+            assert torch.equal(got[b, :, :L].cpu().double(), ref.gathered(pool.value[n], pool.table[b], L))
+    del k, v
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n", [1, 20, 100])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_queries_broadcast_over_heads_or_tokens(attn, n, e4m3):  # noqa: F811
+    """Views of stride 0, and tokens closer together than heads."""
+    Hq, Hkv, d, page, L = 4, 2, 128, 64, 300
+    pool = Pool(1, Hkv, page, d, [L], e4m3, seed=n)
+    where, scales = pool.cuda()
+    args = (*where, bounds([n]).cuda(), ints([L]).cuda())
+    for q in (normal((n, 1, d), 1).cuda().expand(n, Hq, d), normal((1, Hq, d), 2).cuda().expand(n, Hq, d),
+              normal((Hq, n, d), 3).cuda().transpose(0, 1)):
+        got, want = attn.attn_paged(q, *args, **scales), attn.attn_paged(q.contiguous(), *args, **scales)
+        ok(attn)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
