@@ -394,7 +394,8 @@ def attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *, k_scale=None, 
     with _on(dev):
         rc = binding.lib().attn_paged(q.data_ptr(), _strides(q), cache, batch, o.data_ptr(), lse.data_ptr(), Hq,
                                       d ** -0.5 if scale is None else scale, 1 if causal else 0,
-                                      -1 if window_left is None else window_left, ws, ws_bytes, _stream(stream, dev))
+                                      -1 if window_left is None else max(-1, min(window_left, 1 << 30)), ws, ws_bytes,
+                                      _stream(stream, dev))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_paged")
     return o, lse

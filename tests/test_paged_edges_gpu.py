@@ -371,3 +371,46 @@ def test_queries_broadcast_over_heads_or_tokens(attn, n, e4m3):  # noqa: F811
         got, want = attn.attn_paged(q, *args, **scales), attn.attn_paged(q.contiguous(), *args, **scales)
         ok(attn)
         assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+# ------------------------------------------------------------------ windows beyond an int, graphs that allocate
+@pytest.mark.parametrize("window", [1 << 30, 1 << 31, 1 << 32, (1 << 32) + 5, (1 << 63) - 1, -(1 << 32), -(1 << 40) + 3])
+def test_windows_past_32_bits_are_no_limit(attn, window):  # noqa: F811
+    pool = Pool(1, 2, 32, 64, [300], False, seed=1)
+    where, _ = pool.cuda()
+    args = (normal((20, 4, 64), 2).cuda(), *where, bounds([20]).cuda(), ints([300]).cuda())
+    want, got = attn.attn_paged(*args), attn.attn_paged(*args, window_left=window)
+    ok(attn)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_two_graphs_that_take_their_own_memory(attn, e4m3):  # noqa: F811
+    """A decoding step and a chunk, captured without outputs or workspaces, replayed in turn while the
+    lengths move: the same bits as calls outside a graph."""
+    Hq, Hkv, d, page, most = 8, 2, 128, 32, 500
+    pool = Pool(2, Hkv, page, d, [most, most], e4m3, seed=8)
+    where, scales = pool.cuda()
+    f = attn.rope_inv_freq(d)[0]
+    new = normal((300, Hq + 2 * Hkv, d), 9).cuda()
+    graphs = []
+    for n in (1, 120):
+        x, kv_len, cu = new[:2 * n].clone(), ints([n, n]).cuda(), bounds([n, n]).cuda()
+
+        def step(x=x, kv_len=kv_len, cu=cu):
+            q = attn.attn_cache_write(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], *where, cu, kv_len, **scales, inv_freq=f, q=x[:, :Hq])
+            return attn.attn_paged(q, *where, cu, kv_len, **scales)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, step, kv_len, out, n))
+    for at in (200, 333, 480):
+        for graph, step, kv_len, out, n in graphs:
+            kv_len.copy_(ints([at, at - 70]))
+            graph.replay()
+            got = [t.clone() for t in out]
+            want = step()
+            ok(attn)
+            assert all(torch.equal(g, w) for g, w in zip(got, want))
