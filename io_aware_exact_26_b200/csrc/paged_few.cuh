@@ -39,9 +39,10 @@
 // p2's 256.  So a value is exact down to 2^-35 of its row's largest magnitude and off by at
 // most 2^-43 of it below.  (Two parts, p1 unscaled, lose bits from 2^-10 of it on.)  The parts are
 // columns of the same product (the MMA thread, which issues 8 small instructions per P V,
-// bounds an e4m3 tile, so S should take few), and the softmax thread adds them up; the scales
-// 2^e of a query row and of its key multiply the sum.  V is widened to bf16, as its products
-// with P need.
+// bounds an e4m3 tile, so S should take few), and the softmax thread adds them up, the last two
+// (at d = 64) only where a row of the piece has a value that the first two do not hold: they
+// hold all down to 2^-13 of the largest magnitude.  The scales 2^e of a query row and of its key
+// multiply the sum.  V is widened to bf16, as its products with P need.
 #pragma once
 #include "paged.cuh"
 
@@ -65,6 +66,10 @@ struct FewCfg {
   static constexpr int QST = 2;
   static constexpr int NS = K8 ? 4 * NR : NQ;      // columns of S^T; K8: part i of row r in column i NR + r
   static constexpr int kQ8 = K8 ? NS * 128 : 0;    // the parts, 128-byte rows
+  // Columns of the last two parts are read only where a row needs them.  64 x 4K, pages of 64, one
+  // head: 170 -> 150 us at d = 64; else the branch costs more than the columns (d = 128: 183 ->
+  // 187; 8 rows of d = 64, 64 x 8K: 182 -> 185; 12 of d = 128, 16 x 8K: 86 -> 93).
+  static constexpr bool kSkipParts = K8 && NR == 4 && D == 64;
   static constexpr int KSK = K8 ? 4 : D == 128 ? 3 : 6;
   static constexpr int KSV = KV8 ? (D == 128 ? 2 : 3) : KSK;
   // S(g) completes behind PV(g - SA), so P(g) may take the buffer of P(g - NP) for NP >= SA
@@ -107,6 +112,7 @@ struct FewShared : PagedPipe {
   float wsum[2][2][4][NR];             // [piece parity][group][warp]
   float base[2][2][NR];                // [piece parity][group] exponent bases
   alignas(16) float cq[4][NR];                    // K8: 2^e of the query rows, by piece % 4
+  alignas(8) uint8_t wide[4][8];                  // K8: whether the rows of a widening warp need four parts, likewise
   int vote[2][2][4];                   // [group][parity of its steps][warp]
   // By step % 4: S runs up to 3 steps ahead of P V, so a group may finish two of its steps
   // before the MMA warp looks at the first (a parity wait tells two successive phases apart).
@@ -184,29 +190,33 @@ __device__ __forceinline__ void few_tmem_st(uint32_t addr, const float (&f)[NR])
 // Scale between part i of Q and part i + 1 (see the head of this file).
 __host__ __device__ constexpr float few_part_step(int i) { return i == 1 ? 262144.f : 16.f; }
 
-// Scores of this thread's key from the four parts of Q, smallest first: 16 columns per trip to TMEM.
-template <int NR>
+// Scores of this thread's key from the first PARTS parts of Q, smallest first: up to 16 columns per
+// trip to TMEM.
+template <int NR, int PARTS>
 __device__ __forceinline__ void few_scores(uint32_t addr, float (&x)[NR]) {
-  constexpr int PER = 16 / NR;                       // parts per trip
+  constexpr int PER = PARTS * NR <= 16 ? PARTS : 16 / NR;      // parts per trip
 #pragma unroll
-  for (int part = 4 - PER; part >= 0; part -= PER) {
-    float t[16];
-    few_tmem_ld<16>(addr + part * NR, t);
+  for (int part = PARTS - PER; part >= 0; part -= PER) {
+    float t[PER * NR];
+    few_tmem_ld<PER * NR>(addr + part * NR, t);
 #pragma unroll
     for (int i = PER - 1; i >= 0; --i)
 #pragma unroll
       for (int q = 0; q < NR; ++q)
-        x[q] = part + i == 3 ? t[i * NR + q] : fmaf(x[q], 1.f / few_part_step(part + i), t[i * NR + q]);
+        x[q] = part + i == PARTS - 1 ? t[i * NR + q] : fmaf(x[q], 1.f / few_part_step(part + i), t[i * NR + q]);
   }
 }
 
 // 2^(byte - 127), also for byte 0 (subnormal).
 __device__ __forceinline__ float e8m0_value(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
 
-// Q of a piece in four e4m3 parts (see the head of this file), row scales to cq.
+// Q of a piece in four e4m3 parts (see the head of this file), row scales to cq, and to wide whether
+// the first two leave anything.
 template <class C>
-__device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float* cq, int wt) {
+__device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float* cq, uint8_t* wide, int wt) {
   constexpr int CPR = C::D / 8;                      // 8-value chunks per row, one per lane
+  static_assert(C::kWiden == 8, "a byte of `wide` per warp");
+  bool more = false;
   for (int x = wt; x < C::NR * CPR; x += 32 * C::kWiden) {
     const int r = x / CPR, c = x % CPR;
     const uint4 raw = *reinterpret_cast<const uint4*>(q + (c >> 3) * C::kQBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -238,12 +248,17 @@ __device__ __forceinline__ void few_split_q(const uint8_t* q, uint8_t* q8, float
         f[i] = (f[i] - g.x) * few_part_step(part);
         f[i + 1] = (f[i + 1] - g.y) * few_part_step(part);
         w[i >> 1] = two;
+        if (part == 1) more |= f[i] != 0.f || f[i + 1] != 0.f;
       }
       const int pr = part * C::NR + r;
       *reinterpret_cast<uint2*>(q8 + pr * 128 + (((c >> 1) ^ (pr & 7)) << 4) + (c & 1) * 8) =
           make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     }
     if (c == 0) cq[r] = e8m0_value(static_cast<uint32_t>(e + 127));
+  }
+  if constexpr (C::kSkipParts) {
+    more = __any_sync(0xffffffffu, more);
+    if ((wt & 31) == 0) wide[wt >> 5] = more;
   }
 }
 
@@ -362,7 +377,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
     if constexpr (KV8) {
       const int wt = threadIdx.x - 352;
       paged_widen<C>(sh, m, wt, lane, [&](int k, int qs) {
-        few_split_q<C>(m.q + qs * C::kQTile, sQ8 + qs * C::kQ8, sh.cq[k & 3], wt);
+        few_split_q<C>(m.q + qs * C::kQTile, sQ8 + qs * C::kQ8, sh.cq[k & 3], sh.wide[k & 3], wt);
       });
     }
   } else {
@@ -394,6 +409,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
         ls[q] = 0.f;
       }
       const int g_end = gs + w.n;
+      [[maybe_unused]] bool wide = !C::kSkipParts;              // K8: Q takes four parts
       for (int g = gs + ((gs ^ x2) & 1); g < g_end; g += 2) {
         const int par = (g >> 1) & 1;                           // parity of the group's steps
         ok = __all_sync(0xffffffffu, tile_done_wait(sh.k_done, g));
@@ -406,7 +422,12 @@ __global__ void __launch_bounds__(FewCfg<D, KV8, NR>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < NR; ++q) x[q] *= p.cs;
         } else {
-          few_scores<NR>(lane_base + (g & 3) * C::NS, x);
+          if (C::kSkipParts && g < gs + 2) {                    // the group's first step of the piece
+            const uint2 f = *reinterpret_cast<const uint2*>(sh.wide[uq & 3]);
+            wide = (f.x | f.y) != 0;
+          }
+          if (wide) few_scores<NR, 4>(lane_base + (g & 3) * C::NS, x);
+          else few_scores<NR, 2>(lane_base + (g & 3) * C::NS, x);
           // The scales of key and row are multiplied first: a large one and a small one cancel
           // before either meets the sum, which alone can pass fp32 with the row's.
           const float c = p.cs * e8m0_value(m.kscale[(g & 7) * 128 + row]);

@@ -414,3 +414,21 @@ def test_two_graphs_that_take_their_own_memory(attn, e4m3):  # noqa: F811
             want = step()
             ok(attn)
             assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", FEW)
+def test_wide_and_narrow_queries_in_turn_on_one_sm(attn, G, n, d):  # noqa: F811
+    """700 short sequences, several to an SM, every third with a wide query: each gets the parts that it needs."""
+    B, Hkv, page, L = 700, 1, 32, 20
+    pool = Pool(B, Hkv, page, d, [L] * B, True, seed=G)
+    codes = pool.store["k"][..., 5]
+    pool.store["k"][..., 5] = torch.where(codes != 0x7f, codes & 1, codes)
+    pool.value["k"] = ref.widened(pool.store["k"], pool.store["ks"])
+    q = normal((B * n, G, d), 3 + G)
+    wide = (torch.arange(B) % 3 == 0).repeat_interleave(n)
+    q[..., 5] = torch.where(wide.unsqueeze(1), q[..., 5].float() * 2.0 ** 17, q[..., 5].float()).to(torch.bfloat16)
+    where, scales = pool.cuda()
+    got = attn.attn_paged(q.cuda(), *where, bounds([n] * B).cuda(), ints([L] * B).cuda(), **scales)
+    ok(attn)
+    check_attention(got, ref.attend(q, pool.value["k"], pool.value["v"], pool.table, bounds([n] * B), [L] * B, d ** -0.5))
