@@ -68,8 +68,10 @@ typedef struct {
  * turned by the angle pos * inv_freq[i] and multiplied by mscale, the rest is copied:
  *     a' = m (a cos - b sin),  b' = m (b cos + a sin),
  * with (a, b) = (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) if interleaved.  The angle is
- * formed and reduced in fp64 (exact to 2^-24 of a turn for any int32 position), sine,
- * cosine and the rotation are fp32, rounded once at the end.
+ * formed and reduced in fp64, so that it is off by at most 2^-26 of a turn and
+ * 3 * 2^-53 of its own size (together 2^-24 of a turn up to 2^27 turns: 1 radian per
+ * position up to position 8.4e8); sine, cosine and the rotation are fp32, rounded once at
+ * the end.
  *   inv_freq : fp64 [rot / 2], radians per position (scaled for long contexts as the
  *              caller likes: any frequencies are taken)
  *   rot      : a multiple of 16, 16 <= rot <= d
@@ -94,7 +96,7 @@ typedef struct {
  *   inverse   : 0 = the rotation; 1 = its transpose, which maps the gradient of the
  *               outputs to the gradient of the inputs (mscale applies to both)
  * q_out may be q and k_out may be k (same strides); otherwise inputs and outputs must not
- * overlap.  One kernel. */
+ * overlap.  B * N is below 2^31, Hq + Hkv at most 65535.  One kernel. */
 int attn_rope(const void* q, const attn_strides_t* q_strides, void* q_out, const attn_strides_t* q_out_strides, int Hq,
               const void* k, const attn_strides_t* k_strides, void* k_out, const attn_strides_t* k_out_strides, int Hkv,
               int dtype, int B, int N, int d, const int* positions, long long pos_batch_stride,
@@ -111,7 +113,7 @@ int attn_rope(const void* q, const attn_strides_t* q_strides, void* q_out, const
  * the row's largest finite magnitude to at most 448 (-127 <= e <= 120) and e + 127 as the
  * scale byte; rotated rows are quantised from fp32.  Infinities become +-448, NaN stays.
  * Two tokens of one call must not share a cache row.  Rows of the pages that no token
- * maps to keep their contents.  One kernel. */
+ * maps to keep their contents.  Hq + 2 Hkv is at most 65535.  One kernel. */
 int attn_cache_write(const attn_cache_t* cache, const attn_batch_t* batch,
                      const void* k, const attn_strides_t* k_strides, const void* v, const attn_strides_t* v_strides,
                      const attn_rope_t* rope, const void* q, const attn_strides_t* q_strides,
@@ -121,7 +123,7 @@ int attn_cache_write(const attn_cache_t* cache, const attn_batch_t* batch,
  * to k_out, v_out : bf16 [B][Hkv][N][d] -- the layout of attn_fwd and attn_decode.  Rows
  * behind a sequence's length keep their contents.  e4m3 rows become code * 2^(byte - 127),
  * which bf16 holds exactly (down to its subnormals).  batch->cu_q is not used and may be
- * NULL.  One kernel. */
+ * NULL.  B * Hkv is at most 65535 and N at most 2^30.  One kernel. */
 int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* k_out, void* v_out, int N, void* stream);
 
 /* Attention of the new tokens over the cache (which holds their own K and V too):
@@ -138,13 +140,20 @@ int attn_cache_read(const attn_cache_t* cache, const attn_batch_t* batch, void* 
  * its row's largest magnitude and to 2^-43 of that magnitude below.  Sums and softmax
  * statistics are fp32; P is rounded to bf16.
  * Masked scores never reach the sums, whatever the cache holds there; values of V at
- * positions below kv_len[b] have to be finite in the rows' visible 128-key tiles.  An
- * infinite query value counts as NaN over an e4m3 cache.
+ * positions below kv_len[b] have to be finite in every 128-key tile that some row of the
+ * sequence sees.  A row that sees a NaN score or one of +infinity is NaN; so may be a row
+ * with an infinite query value.
  * The cache rows of this call's tokens must have been written before, on this stream or
  * ordered before it.
  * The keys are shared out evenly over the SMs by each CTA from cu_q and kv_len on the
  * device, so one captured launch serves any lengths; results do not depend on which SM
  * runs first, and equal calls give equal bits.
+ * Lengths being on the device, the host picks one of three kernels by the mean of query
+ * rows per sequence, Hq / Hkv * T / B, with T counting padding and B counting sequences
+ * without new tokens.  Any of them is right for any batch, but one for few rows takes a long
+ * chunk a few rows at a time: 256 sequences of which one has 256 new tokens over 4096 (32
+ * query heads to 8, d = 128, bf16) take 263 us, that one alone 47.  Where long chunks meet
+ * mostly empty or padded slots, leave those slots out or give the chunks their own call.
  * Workspace: attn_paged_workspace_size(...) bytes (queried with the same device current;
  * it does not depend on lengths), or NULL: the library takes it with cudaMallocAsync /
  * cudaFreeAsync on `stream`.  It is overwritten; calls that may overlap need one each.

@@ -365,6 +365,8 @@ def attn_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, *, k_scale=None, 
     Token t of sequence b has position kv_len[b] - cu_q[b+1] + t and sees the cached keys up
     to it (causal), no further back than window_left positions (None or negative: no limit).
     Rows that see no key get o = 0 and lse = -inf; rows from cu_q[B] on are left alone.
+    The kernel is picked by the mean number of new tokens, T / B: a long chunk among mostly
+    empty sequences is better called without them (include/attn_paged.h).
     workspace: a device tensor of attn_paged_workspace_size(T, B, Hq, Hkv, d) bytes, one for
     each call that may run at the same time; None lets the library allocate it on the stream.
     """
