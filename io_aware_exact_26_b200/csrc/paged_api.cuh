@@ -161,8 +161,8 @@ bool make_q_map(CUtensorMap* m, const void* q, const attn_strides_t* st, int T, 
 // against the 128-row kernel, us, 16 sequences of 8K at 4 heads to 8, and 32 of 512:
 //   bf16, d = 128:  8 rows 77 : 73, 24 : 21;  32 rows 143 : 75, 71 : 25;  4 rows 20 : 25 at 32 of 512
 //   bf16, d = 64:   8 rows 52 : 64, 24 : 20;  16 rows 69 : 64, 35 : 22
-//   e4m3, d = 64:   8 rows 57 : 78, 32 : 25;  16 rows 93 : 77, 51 : 28
-//   e4m3, d = 128:  16 rows 87 : 119, 47 : 34;  32 rows 147 : 121, 79 : 37
+//   e4m3, d = 64:   8 rows 57 : 78, 33 : 24;  16 rows 93 : 77, 51 : 28
+//   e4m3, d = 128:  16 rows 92 : 119, 48 : 34;  32 rows 147 : 121, 79 : 37
 // The other side is the faster one past these limits on long caches of one query head to
 // a cache head (d = 64, 16 tokens on 65K: bf16 176 : 238; e4m3, d = 128, 32 tokens: 338 : 455).
 constexpr int few_rows_limit(int d, bool kv8) { return d == 64 ? 8 : kv8 ? 16 : 4; }
