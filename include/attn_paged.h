@@ -23,8 +23,8 @@
  * may hold anything.  An entry outside [0, num_pages), or a position beyond max_pages pages,
  * is never followed: the write of that token is skipped, reads see zeros there, attention
  * takes the sequence as max_pages pages long, and attn_get_device_status() reports
- * ATTN_ERR_DEVICE_PAGE once the work has run.  kv_len is below 2^30; a negative one counts
- * as 0.
+ * ATTN_ERR_DEVICE_PAGE once the work has run (not for a sequence without new tokens, which
+ * the write and the attention pass over).  kv_len is below 2^30; a negative one counts as 0.
  */
 #ifndef ATTN_B200_PAGED_H
 #define ATTN_B200_PAGED_H
